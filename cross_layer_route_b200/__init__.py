@@ -24,7 +24,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librr.so")
 
 RR_OK, RR_EINVAL, RR_ESTATE, RR_ENOMEM, RR_ECUDA, RR_EDEVICE, RR_ECAPACITY = range(7)
-RR_F32, RR_BF16 = 0, 1
+RR_F32, RR_BF16, RR_F16 = 0, 1, 2
+RR_E4M3, RR_E2M1 = 0, 1
 CNT_ROWS, CNT_PAIRS, CNT_ERROR, CNT_ROWS_TOTAL, CNT_PAIRS_TOTAL, CNT_LAYERS, CNT_LAST_LAYER, \
     CNT_DRAW_CAP, CNT_FULL_PAIRS, CNT_FULL_PAIRS_TOTAL, CNT_RETRY_TOTAL = range(11)
 NUM_COUNTERS = 16
@@ -49,6 +50,43 @@ class rr_attn_config(ctypes.Structure):
     _fields_ = [("bh", ctypes.c_int32), ("nq_tokens", ctypes.c_int32), ("nk_tokens", ctypes.c_int32),
                 ("dh", ctypes.c_int32), ("chunk", ctypes.c_int32), ("width", ctypes.c_int32),
                 ("route_stride", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class rr_masked_attn_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "q_heads", "kv_heads", "route_heads", "nq_tokens", "nk_tokens", "dh", "chunk", "width",
+                 "route_stride", "causal", "dtype", "q_offset")] + \
+               [("scale", ctypes.c_float), ("soft_cap", ctypes.c_float)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+
+
+class rr_masked_attn_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("q", "k", "v", "route", "slopes", "doc_q", "doc_k", "prefix", "out", "lse")]
+
+
+class rr_cache_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("pages", "heads", "dh", "chunk", "format")]
+
+
+class rr_cache_pool(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class rr_cache_rows(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cu", ctypes.c_void_p),
+                ("start", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32)]
+
+
+class rr_cached_attn_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "q_tokens", "q_heads", "dtype", "table_width", "table_stride", "width", "route_stride")] + \
+               [("scale", ctypes.c_float), ("soft_cap", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3)]
+
+
+class rr_cached_attn_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "seq_lens", "page_table", "route", "slopes", "out", "lse")]
 
 
 def _load():
@@ -84,6 +122,24 @@ def _load():
     lib.rr_route_layer_static.restype = ctypes.c_int
     lib.rr_sparse_attention.argtypes = [ctypes.POINTER(rr_attn_config), P, P, P, P, P, P]
     lib.rr_sparse_attention.restype = ctypes.c_int
+    ref = ctypes.POINTER
+    lib.rr_masked_attention.argtypes = [ref(rr_masked_attn_config), ref(rr_masked_attn_args), P]
+    lib.rr_masked_attention.restype = ctypes.c_int
+    for name in ("rr_cache_codes_bytes", "rr_cache_scales_bytes"):
+        f = getattr(lib, name)
+        f.argtypes = [ref(rr_cache_config)]
+        f.restype = ctypes.c_size_t
+    for name in ("rr_cache_write", "rr_cache_read"):
+        f = getattr(lib, name)
+        f.argtypes = [ref(rr_cache_config), ref(rr_cache_pool), ref(rr_cache_rows), P, ctypes.c_int64 * 2, P,
+                      ctypes.c_int64 * 2, ctypes.c_int32, P]
+        f.restype = ctypes.c_int
+    lib.rr_cached_attention_workspace_bytes.argtypes = [ref(rr_cache_config), ref(rr_cached_attn_config),
+                                                        ctypes.c_int32]
+    lib.rr_cached_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.rr_cached_attention.argtypes = [ref(rr_cache_config), ref(rr_cache_pool), ref(rr_cached_attn_config),
+                                        ref(rr_cached_attn_args), P, ctypes.c_size_t, P]
+    lib.rr_cached_attention.restype = ctypes.c_int
     lib.rr_status_string.argtypes = [ctypes.c_int]
     lib.rr_status_string.restype = ctypes.c_char_p
     return lib
@@ -196,6 +252,46 @@ def rr_sparse_attention(cfg: rr_attn_config, d_q: int, d_k: int, d_v: int, d_rou
                                     ctypes.c_void_p(stream)), "rr_sparse_attention")
 
 
+def rr_masked_attention(cfg: rr_masked_attn_config, args: rr_masked_attn_args, stream: int) -> None:
+    """Masked attention over a route (include/rr_attention.h)."""
+    _check(_lib.rr_masked_attention(cfg, args, stream), "rr_masked_attention")
+
+
+def rr_cache_codes_bytes(cfg: rr_cache_config) -> int:
+    return int(_lib.rr_cache_codes_bytes(cfg))
+
+
+def rr_cache_scales_bytes(cfg: rr_cache_config) -> int:
+    return int(_lib.rr_cache_scales_bytes(cfg))
+
+
+def rr_cache_write(cfg: rr_cache_config, pool: rr_cache_pool, rows: rr_cache_rows, d_k: int, k_stride, d_v: int,
+                   v_stride, dtype: int, stream: int) -> None:
+    """Quantised store into the paged cache (include/rr_cache.h)."""
+    pair = ctypes.c_int64 * 2
+    _check(_lib.rr_cache_write(cfg, pool, rows, d_k, pair(*k_stride), d_v, pair(*v_stride), dtype, stream),
+           "rr_cache_write")
+
+
+def rr_cache_read(cfg: rr_cache_config, pool: rr_cache_pool, rows: rr_cache_rows, d_k: int, k_stride, d_v: int,
+                  v_stride, dtype: int, stream: int) -> None:
+    """Rows of the paged cache read back (include/rr_cache.h)."""
+    pair = ctypes.c_int64 * 2
+    _check(_lib.rr_cache_read(cfg, pool, rows, d_k, pair(*k_stride), d_v, pair(*v_stride), dtype, stream),
+           "rr_cache_read")
+
+
+def rr_cached_attention_workspace_bytes(cfg: rr_cache_config, attn: rr_cached_attn_config, routed: bool) -> int:
+    return int(_lib.rr_cached_attention_workspace_bytes(cfg, attn, int(bool(routed))))
+
+
+def rr_cached_attention(cfg: rr_cache_config, pool: rr_cache_pool, attn: rr_cached_attn_config,
+                        args: rr_cached_attn_args, workspace: int, workspace_bytes: int, stream: int) -> None:
+    """Attention over the paged cache (include/rr_cache.h)."""
+    _check(_lib.rr_cached_attention(cfg, pool, attn, args, workspace, workspace_bytes, stream),
+           "rr_cached_attention")
+
+
 # ---- convenience wrapper over torch memory --------------------------------
 @dataclass
 class Config:
@@ -272,6 +368,263 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: t
     rr_sparse_attention(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), route.data_ptr(), out.data_ptr(),
                         _stream_handle(stream))
     return out
+
+
+_DTYPES = {torch.float32: RR_F32, torch.bfloat16: RR_BF16, torch.float16: RR_F16}
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _describe(t) -> str:
+    return f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+
+
+class _call_on:
+    """The device and stream of a call: makes the tensors' device current and,
+    where the caller names a stream, that stream too, so that what the call
+    allocates belongs to it.  Yields the stream's handle."""
+
+    def __init__(self, device, stream):
+        self.context = None
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device) if stream \
+                    else torch.cuda.default_stream(device)
+            if stream.device != device:
+                raise ValueError(f"stream: expected a stream of {device}, got one of {stream.device}")
+            self.context = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.context = torch.cuda.device(device)
+        self.device = device
+
+    def __enter__(self) -> int:
+        if self.context is not None:
+            self.context.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *error):
+        if self.context is not None:
+            self.context.__exit__(*error)
+
+
+def _int32(name, t, shape, device):
+    """A contiguous int32 tensor of this shape (None: any size there)."""
+    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) or not t.is_contiguous() \
+            or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected contiguous int32 {shape} on {device}, got {_describe(t)}")
+    return t.data_ptr()
+
+
+def _slopes(t, heads, device):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != device or t.dim() != 1 or t.shape[0] != heads \
+            or not t.is_contiguous():
+        raise ValueError(f"slopes: expected contiguous float32 [{heads}] on {device}, got {_describe(t)}")
+    return t.data_ptr()
+
+
+def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: torch.Tensor, chunk: int,
+                     causal: bool = False, width: int | None = None, scale: float | None = None,
+                     soft_cap: float = 0.0, slopes: torch.Tensor | None = None, doc_q: torch.Tensor | None = None,
+                     doc_k: torch.Tensor | None = None, prefix: torch.Tensor | None = None, q_offset: int = 0,
+                     out: torch.Tensor | None = None, return_lse: bool = False, stream=None):
+    """Attention over a route with capped scores (`soft_cap`), a bias by
+    distance (`slopes` [q_heads] float32), a document mask (`doc_q` [batch,
+    nq_tokens] and `doc_k` [batch, nk_tokens] int32) and a prefix that the
+    causal rule leaves visible (`prefix` [batch] int32); the formulas stand in
+    include/rr_attention.h.
+
+    q [batch, q_heads, nq_tokens, dh], k and v [batch, kv_heads, nk_tokens, dh]:
+    bf16 or f16 on one CUDA device, any strides that are multiples of 8 with dh
+    contiguous.  route: contiguous int32 [batch, route_heads, query chunks,
+    stride] of key-chunk ids, of which the first `width` (default: all) are
+    read.  q_offset: position of query token 0.  Returns (or fills) `out` like
+    q, with return_lse also the float32 [batch, q_heads, nq_tokens] logarithms
+    of the softmax sums."""
+    device, dtype = q.device, q.dtype
+    if q.dim() != 4 or k.dim() != 4 or dtype not in _HALVES or not q.is_cuda:
+        raise ValueError(f"q: expected bf16 or f16 [batch, heads, tokens, dh] on a CUDA device, got {_describe(q)}")
+    batch, q_heads, nq, dh = q.shape
+    kv_heads, nk = k.shape[1], k.shape[2]
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != dtype or t.device != device or t.shape != (batch, kv_heads, nk, dh) or t.stride(3) != 1:
+            raise ValueError(f"{name}: expected {dtype} {(batch, kv_heads, nk, dh)} on {device}, dh contiguous, "
+                             f"got {_describe(t)}")
+    if q.stride(3) != 1:
+        raise ValueError(f"q: expected dh contiguous, got {_describe(q)}")
+    chunks = -(-nq // chunk) if chunk > 0 else 0
+    d_route = _int32("route", route, (batch, None, chunks, None), device)
+    route_heads, stride = route.shape[1], route.shape[3]
+    width = stride if width is None else int(width)
+    if width > stride:
+        raise ValueError(f"width {width} is larger than the route's {stride} entries")
+    if out is not None and (out.dtype != dtype or out.device != device or out.shape != q.shape
+                            or out.stride(3) != 1):
+        raise ValueError(f"out: expected {dtype} {tuple(q.shape)} on {device}, dh contiguous, got {_describe(out)}")
+    if (doc_q is None) != (doc_k is None):
+        raise ValueError("doc_q and doc_k go together")
+    d_slopes = _slopes(slopes, q_heads, device)
+    d_doc_q = None if doc_q is None else _int32("doc_q", doc_q, (batch, nq), device)
+    d_doc_k = None if doc_k is None else _int32("doc_k", doc_k, (batch, nk), device)
+    d_prefix = None if prefix is None else _int32("prefix", prefix, (batch,), device)
+    with _call_on(device, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        lse = torch.empty((batch, q_heads, nq), dtype=torch.float32, device=device) if return_lse else None
+        ints = ctypes.c_int64 * 3
+        cfg = rr_masked_attn_config(batch, q_heads, kv_heads, route_heads, nq, nk, dh, chunk, width, max(stride, 1),
+                                    int(bool(causal)), _DTYPES[dtype], q_offset, 0.0 if scale is None else scale,
+                                    soft_cap, ints(*_strides(q)), ints(*_strides(k)), ints(*_strides(v)),
+                                    ints(*_strides(out)))
+        args = rr_masked_attn_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), d_route, d_slopes, d_doc_q, d_doc_k,
+                                   d_prefix, out.data_ptr(), None if lse is None else lse.data_ptr())
+        rr_masked_attention(cfg, args, handle)
+    return (out, lse) if return_lse else out
+
+
+def _strides(t):
+    """Strides of all but the last dimension; that of a size of one counts nothing."""
+    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride())]
+
+
+def _cache(codes, scales, dh):
+    """(config, pool) of a cache's two arrays, for rows of dh elements."""
+    device = codes.device
+    if codes.dtype != torch.uint8 or not codes.is_cuda or codes.dim() != 5 or codes.shape[2] != 2 \
+            or not codes.is_contiguous():
+        raise ValueError(f"codes: expected contiguous uint8 [pages, heads, 2, chunk, bytes] on a CUDA device, "
+                         f"got {_describe(codes)}")
+    pages, heads, _, chunk, row = codes.shape
+    if row == dh:
+        fmt, groups = RR_E4M3, 1
+    elif 2 * row == dh:
+        fmt, groups = RR_E2M1, dh // 32
+    else:
+        raise ValueError(f"codes: rows of {row} bytes hold no {dh} elements (e4m3: {dh} bytes, e2m1: {dh // 2})")
+    if scales.dtype != torch.uint8 or scales.device != device or scales.shape != (pages, heads, 2, chunk, groups) \
+            or not scales.is_contiguous():
+        raise ValueError(f"scales: expected contiguous uint8 {(pages, heads, 2, chunk, groups)} on {device}, "
+                         f"got {_describe(scales)}")
+    return rr_cache_config(pages, heads, dh, chunk, fmt), rr_cache_pool(codes.data_ptr(), scales.data_ptr())
+
+
+def cache_empty(pages: int, heads: int, chunk: int, dh: int, fmt: str = "e4m3", device=None):
+    """(codes, scales) of a cache of `pages` pages of `chunk` tokens, zeroed
+    (every row reads as zeros); fmt "e4m3" or "e2m1"."""
+    if fmt not in ("e4m3", "e2m1"):
+        raise ValueError(f'fmt: expected "e4m3" or "e2m1", got {fmt!r}')
+    if pages < 0 or heads < 1 or chunk not in (16, 32, 64, 128) or dh not in (64, 128):
+        raise RRError(RR_EINVAL, f"cache_empty(pages={pages}, heads={heads}, chunk={chunk}, dh={dh})")
+    row, groups = (dh, 1) if fmt == "e4m3" else (dh // 2, dh // 32)
+    mk = lambda n: torch.zeros((pages, heads, 2, chunk, n), dtype=torch.uint8, device=device or "cuda")
+    return mk(row), mk(groups)
+
+
+def _rows(rows, cu, start, table, device):
+    d_table = _int32("table", table, (None, None), device)
+    batch, width = table.shape
+    return rr_cache_rows(batch, rows, _int32("cu", cu, (batch + 1,), device),
+                         _int32("start", start, (batch,), device), d_table, width, max(width, 1))
+
+
+def cache_write(codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
+                start: torch.Tensor, table: torch.Tensor, stream=None) -> None:
+    """Quantises keys and values into the paged cache (include/rr_cache.h).
+    codes uint8 [pages, heads, 2, chunk, dh] (e4m3) or [..., dh // 2] (e2m1),
+    scales uint8 [pages, heads, 2, chunk, 1] or [..., dh // 32]; k and v [rows,
+    heads, dh] of one type (f32, bf16, f16), any strides that keep rows 16-byte
+    aligned; rows cu[b]..cu[b+1]-1 are sequence b's at positions start[b]...;
+    table [batch, width]: pages of each sequence's chunks (-1: none)."""
+    device, dtype = codes.device, k.dtype
+    if k.dim() != 3 or dtype not in _DTYPES:
+        raise ValueError(f"k: expected f32, bf16 or f16 [rows, heads, dh], got {_describe(k)}")
+    rows, heads, dh = k.shape
+    cfg, pool = _cache(codes, scales, dh)
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != dtype or t.device != device or t.shape != (rows, cfg.heads, dh) or t.stride(2) != 1:
+            raise ValueError(f"{name}: expected {dtype} {(rows, cfg.heads, dh)} on {device}, dh contiguous, "
+                             f"got {_describe(t)}")
+    batch = _rows(rows, cu, start, table, device)
+    with _call_on(device, stream) as handle:
+        rr_cache_write(cfg, pool, batch, k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), _DTYPES[dtype], handle)
+
+
+def cache_read(codes: torch.Tensor, scales: torch.Tensor, cu: torch.Tensor, start: torch.Tensor,
+               table: torch.Tensor, rows: int, dh: int, dtype: torch.dtype = torch.bfloat16,
+               out: tuple | None = None, stream=None):
+    """The cached keys and values of a ragged batch, as (k, v) [rows, heads,
+    dh] of `dtype`; see cache_write for the arguments.  Rows that belong to no
+    sequence are not written: they keep what `out` (a pair of tensors to fill)
+    held, and are unspecified without it."""
+    device = codes.device
+    cfg, pool = _cache(codes, scales, dh)
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype: expected float32, bfloat16 or float16, got {dtype}")
+    shape = (rows, cfg.heads, dh)
+    batch = _rows(rows, cu, start, table, device)
+    for name, t in zip("kv", out or ()):
+        if t.dtype != dtype or t.device != device or t.shape != shape or t.stride(2) != 1:
+            raise ValueError(f"out {name}: expected {dtype} {shape} on {device}, dh contiguous, got {_describe(t)}")
+    with _call_on(device, stream) as handle:
+        k, v = out if out is not None else (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        rr_cache_read(cfg, pool, batch, k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), _DTYPES[dtype], handle)
+    return k, v
+
+
+def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor,
+                     table: torch.Tensor, route: torch.Tensor | None = None, width: int | None = None,
+                     scale: float | None = None, soft_cap: float = 0.0, slopes: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, return_lse: bool = False,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's newest tokens over the paged cache
+    (include/rr_cache.h).  q [batch, q_tokens, q_heads, dh] bf16 or f16, dh
+    contiguous; seq_lens [batch] int32: cached tokens, the query tokens among
+    them; table [batch, width] int32; route: None (every chunk) or contiguous
+    int32 [batch, cache heads, stride] of chunk ids, of which the first `width`
+    are read.  Returns (or fills) out like q, contiguous, with return_lse also
+    float32 [batch, q_tokens, q_heads].  `workspace`: uint8 device memory of
+    rr_cached_attention_workspace_bytes, for callers that hold their own; two
+    calls that can run at once need one each."""
+    device, dtype = codes.device, q.dtype
+    if q.dim() != 4 or dtype not in _HALVES or q.device != device or q.stride(3) != 1:
+        raise ValueError(f"q: expected bf16 or f16 [batch, tokens, heads, dh] on {device}, dh contiguous, "
+                         f"got {_describe(q)}")
+    batch, q_tokens, q_heads, dh = q.shape
+    cfg, pool = _cache(codes, scales, dh)
+    d_table = _int32("table", table, (batch, None), device)
+    stride = 1
+    d_route = None
+    if route is not None:
+        d_route = _int32("route", route, (batch, cfg.heads, None), device)
+        stride = route.shape[2]
+    width = (stride if route is not None else 0) if width is None else int(width)
+    if route is None and width:
+        raise ValueError("width goes with a route")
+    if width > stride:
+        raise ValueError(f"width {width} is larger than the route's {stride} entries")
+    if out is not None and (out.dtype != dtype or out.device != device or out.shape != q.shape
+                            or not out.is_contiguous()):
+        raise ValueError(f"out: expected contiguous {dtype} {tuple(q.shape)} on {device}, got {_describe(out)}")
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != device
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected contiguous uint8 on {device}, got {_describe(workspace)}")
+    table_width = table.shape[1]
+    attn = rr_cached_attn_config(batch, q_tokens, q_heads, _DTYPES[dtype], table_width, max(table_width, 1), width,
+                                 max(stride, 1), 0.0 if scale is None else scale, soft_cap,
+                                 (ctypes.c_int64 * 3)(*_strides(q)))
+    d_lens, d_slopes = _int32("seq_lens", seq_lens, (batch,), device), _slopes(slopes, q_heads, device)
+    need = rr_cached_attention_workspace_bytes(cfg, attn, route is not None)
+    with _call_on(device, stream) as handle:
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype, device=device)
+        lse = torch.empty((batch, q_tokens, q_heads), dtype=torch.float32, device=device) if return_lse else None
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        args = rr_cached_attn_args(q.data_ptr(), d_lens, d_table, d_route, d_slopes, out.data_ptr(),
+                                   None if lse is None else lse.data_ptr())
+        rr_cached_attention(cfg, pool, attn, args, None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel(), handle)
+    return (out, lse) if return_lse else out
 
 
 class RouteLedger:
@@ -396,6 +749,42 @@ class RouteLedger:
                              f"got {tuple(q.shape)} / {tuple(k.shape)}")
         ids = self.device_view()["ids"]
         return sparse_attention(q, k, v, ids, chunk, causal=c.causal, width=c.k, out=out, stream=stream)
+
+    def _route_of(self, heads: int, chunk: int, nq_tokens: int, nk_tokens: int):
+        """The ledger's ids in place, as [batch, route heads, query chunks, c]:
+        its bh heads are `heads` route heads of each batch entry."""
+        c = self.cfg
+        if heads < 1 or c.bh % heads != 0:
+            raise ValueError(f"route_heads: expected a divisor of the ledger's {c.bh} heads, got {heads}")
+        if -(-nq_tokens // chunk) != c.nq or -(-nk_tokens // chunk) > c.nk:
+            raise ValueError(f"expected {c.nq} query chunks and at most {c.nk} key chunks of {chunk} tokens, got "
+                             f"{nq_tokens} and {nk_tokens} tokens")
+        return self.device_view()["ids"].view(c.bh // heads, heads, c.nq, c.c)
+
+    def masked_attention(self, q, k, v, chunk: int, route_heads: int | None = None, **options):
+        """masked_attention over the ledger's current routes, read in place:
+        q [batch, q_heads, nq_tokens, dh], k and v [batch, kv_heads, nk_tokens,
+        dh] of the same layer, the last chunk possibly short; route_heads
+        (default: kv_heads) of the ledger's heads belong to each batch entry.
+        The ledger's causal rule is applied at token level; options as there."""
+        if "causal" in options or "width" in options:
+            raise ValueError("causal and width are the ledger's")
+        heads = k.shape[1] if route_heads is None else route_heads
+        ids = self._route_of(heads, chunk, q.shape[2], k.shape[2])
+        return masked_attention(q, k, v, ids, chunk, causal=self.cfg.causal, width=self.cfg.k, **options)
+
+    def cached_attention(self, codes, scales, q, seq_lens, table, **options):
+        """cached_attention over the ledger's current routes, read in place: a
+        ledger of one query chunk (nq = 1) whose heads are the cache's heads of
+        each sequence, batch-major."""
+        c, heads = self.cfg, codes.shape[1]
+        if c.nq != 1 or c.bh != q.shape[0] * heads:
+            raise ValueError(f"expected a ledger of one query chunk for {q.shape[0]} x {heads} heads, got nq {c.nq}, "
+                             f"bh {c.bh}")
+        if "route" in options or "width" in options:
+            raise ValueError("route and width are the ledger's")
+        ids = self.device_view()["ids"].view(q.shape[0], heads, c.c)
+        return cached_attention(codes, scales, q, seq_lens, table, route=ids, width=c.k, **options)
 
     def layer(self, qc, kc, layer: int, stream=None):
         """Layer l of a sequence: an anchor at l == 0, else rr_relay_layer

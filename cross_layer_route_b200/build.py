@@ -14,8 +14,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librr.so")
 SOURCES = ["rr_api.cu", "rr_route_simt.cu", "rr_route_tc.cu", "rr_select_tc.cu", "rr_relay.cu", "rr_noalloc.cu",
-           "rr_attention.cu"]
-HEADERS = ["rr_device.cuh", "rr_internal.h", "rr_tc.cuh"]
+           "rr_attention.cu", "rr_masked.cu",
+           "rr_cache.cu", "rr_cached.cu"]
+HEADERS = ["rr_device.cuh", "rr_internal.h", "rr_tc.cuh", "rr_frag.cuh", "rr_masked.cuh", "rr_cache.cuh"]
 
 
 def nvcc() -> str:
@@ -35,7 +36,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + \
-        [os.path.join(ROOT, "include", h) for h in ("rr.h", "rr_attention.h")]
+        [os.path.join(ROOT, "include", h) for h in ("rr.h", "rr_attention.h", "rr_cache.h")]
     return any(os.path.getmtime(p) > t for p in deps)
 
 

@@ -1,0 +1,360 @@
+// rr_masked.cu -- masked attention over a route (declared in
+// include/rr_attention.h): the entry point and the kernel on mma.sync.
+//
+// One CTA = up to 64 rows of a unit (rr_masked.cuh), 16 rows per warp, so the
+// query heads that share a key head read its chunks once.  Keys are visited in
+// tiles of 64 slots of the concatenated route (a tile holds several chunks of
+// 16 or 32, or half a chunk of 128), staged by cp.async two tiles deep into
+// rows padded by 16 bytes; slots past the route are filled with zeros and
+// masked.  S = q K^T, the softmax and O += P V as in rr_attention.cu, with
+//   x = s2 tanh(s1 s) or s1 s           (base-2 scores)
+//   x -= slope (|pos - key| - near)      near: the row's nearest visible key
+//   x = -inf where the masks say so, looked at per element only in tiles that
+//       are not fully visible to the unit.
+// A masked key has weight exactly zero; only a masked value row that holds an
+// infinity or a NaN could reach a result then, as 0 * NaN, and rows with such
+// accumulators are computed again on their own (row_alone).
+#include <cuda_runtime.h>
+
+#include "rr_masked.cuh"
+
+namespace rr_masked {
+
+using namespace rr_attn;
+
+constexpr int kSlots = 64;      // key slots per tile
+constexpr int kMaxWarps = 4;    // 16 rows each
+
+template <int DH>
+struct Shape {
+    static constexpr int kRow = DH + 8;
+    static constexpr int kTile = kSlots * kRow;
+    static constexpr int kHead = kMaxWidth * 4 + 16;            // list and its length
+    static constexpr int kMeta = 2 * kSlots * 8;                // {position, document} per slot, two stages
+    static constexpr int kSmem = kHead + kMeta + 4 * kTile * 2;
+};
+
+template <typename T, int DH>
+__device__ __forceinline__ void stage_tile(const Masked &p, const Unit &u, const int32_t *list, int slots, int tile,
+                                           const T *k, const T *v, T *sk, T *sv, int2 *meta) {
+    constexpr int kRow = Shape<DH>::kRow;
+    for (int idx = threadIdx.x; idx < kSlots * DH / 8; idx += blockDim.x) {
+        const int r = idx / (DH / 8), c = (idx % (DH / 8)) * 8;
+        const int slot = tile * kSlots + r;
+        int s = -1;
+        if (slot < slots) s = ((list[slot >> p.shift] & kChunkId) << p.shift) + (slot & (p.c.chunk - 1));
+        if (s >= p.c.nk_tokens) s = -1;
+        const int64_t at = s < 0 ? 0 : s;
+        const int bytes = s < 0 ? 0 : 16;
+        cp_async16_zfill(smem_u32(sk + r * kRow + c), k + at * p.c.k_stride[2] + c, bytes);
+        cp_async16_zfill(smem_u32(sv + r * kRow + c), v + at * p.c.v_stride[2] + c, bytes);
+        if (c == 0)
+            meta[r] = make_int2(s, s >= 0 && p.a.doc_k ? p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] : 0);
+    }
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(const __grid_constant__ Masked p) {
+    using S = Shape<DH>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    int32_t *s_list = reinterpret_cast<int32_t *>(smem);
+    int32_t *s_n = s_list + kMaxWidth;
+    int2 *s_meta = reinterpret_cast<int2 *>(smem + S::kHead);              // [2][kSlots]
+    T *s_k = reinterpret_cast<T *>(smem + S::kHead + S::kMeta);            // [2][kSlots][kRow]
+    T *s_v = s_k + 2 * S::kTile;
+
+    const Unit u = unit_of(p, blockIdx.x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int n_list = build_list(p, u, s_list, s_n);
+    const int slots = n_list << p.shift;
+    const int n_tiles = (slots + kSlots - 1) / kSlots;
+
+    const T *k = static_cast<const T *>(p.a.k) + u.b * p.c.k_stride[0] + u.kv_head * p.c.k_stride[1];
+    const T *v = static_cast<const T *>(p.a.v) + u.b * p.c.v_stride[0] + u.kv_head * p.c.v_stride[1];
+    if (n_tiles > 0) stage_tile<T, DH>(p, u, s_list, slots, 0, k, v, s_k, s_v, s_meta);
+    cp_async_commit();
+
+    // This lane's two rows.  The 16 rows of a warp belong to one head (chunks
+    // are multiples of 16); rows past the unit or past its tokens are computed
+    // on zeros and not stored.
+    const int row0 = (u.tile * kMaxWarps + warp) * 16;
+    const int head = u.route_head * p.group + min(row0 >> p.shift, p.group - 1);
+    const int tok0 = (row0 & (p.c.chunk - 1)) + g;                 // within the chunk; and tok0 + 8
+    const bool in_unit = (row0 >> p.shift) < p.group;
+    const bool ok0 = in_unit && tok0 < u.tokens, ok1 = in_unit && tok0 + 8 < u.tokens;
+    const int pos0 = u.p_first + tok0, pos1 = pos0 + 8;
+    const int64_t token = ((int64_t)u.i << p.shift) + tok0;
+    uint32_t qf[DH / 16][4];
+    {
+        const T *q = static_cast<const T *>(p.a.q) + u.b * p.c.q_stride[0] + head * p.c.q_stride[1];
+        const uint32_t *q0 = reinterpret_cast<const uint32_t *>(q + token * p.c.q_stride[2]);
+        const uint32_t *q1 = reinterpret_cast<const uint32_t *>(q + (token + 8) * p.c.q_stride[2]);
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            qf[kk][0] = ok0 ? q0[kk * 8 + t] : 0u;
+            qf[kk][1] = ok1 ? q1[kk * 8 + t] : 0u;
+            qf[kk][2] = ok0 ? q0[kk * 8 + 4 + t] : 0u;
+            qf[kk][3] = ok1 ? q1[kk * 8 + 4 + t] : 0u;
+        }
+    }
+    const bool docs = p.a.doc_q != nullptr, bias = p.a.slopes != nullptr, cap = p.c.soft_cap > 0.f;
+    int doc0 = -1, doc1 = -1;
+    if (docs) {
+        const int32_t *dq = p.a.doc_q + (size_t)u.b * p.c.nq_tokens + token;
+        if (ok0) doc0 = dq[0];
+        if (ok1) doc1 = dq[8];
+    }
+    float slope = 0.f;
+    int near0 = 0, near1 = 0;
+    if (bias) {
+        slope = p.a.slopes[head] * kLog2e;
+        near0 = nearest(p, u, s_list, n_list, pos0, doc0, t, 4);
+        near1 = nearest(p, u, s_list, n_list, pos1, doc1, t, 4);
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            near0 = min(near0, __shfl_xor_sync(kFull, near0, d));
+            near1 = min(near1, __shfl_xor_sync(kFull, near1, d));
+        }
+        if (near0 == INT_MAX) near0 = 0;
+        if (near1 == INT_MAX) near1 = 0;
+    }
+
+    float o[DH / 8][4];
+#pragma unroll
+    for (int nd = 0; nd < DH / 8; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const int lm_row = lane & 7, lm_mat = lane >> 3;
+    const int per_tile = max(1, kSlots >> p.shift);   // list entries a tile spans
+
+    for (int e = 0; e < n_tiles; ++e) {
+        const int st = e & 1;
+        if (e + 1 < n_tiles)
+            stage_tile<T, DH>(p, u, s_list, slots, e + 1, k, v, s_k + (st ^ 1) * S::kTile, s_v + (st ^ 1) * S::kTile,
+                              s_meta + (st ^ 1) * kSlots);
+        cp_async_commit();
+        cp_async_wait_one();
+        __syncthreads();
+        const T *sk = s_k + st * S::kTile;
+        const T *sv = s_v + st * S::kTile;
+        const int2 *meta = s_meta + st * kSlots;
+        const int first = (e * kSlots) >> p.shift;
+        bool full = (e + 1) * kSlots <= slots;
+        for (int i = 0; i < per_tile && full; ++i) full = (s_list[first + i] & kChunkFull) != 0;
+
+        float s[kSlots / 8][4];
+#pragma unroll
+        for (int n = 0; n < kSlots / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+#pragma unroll
+            for (int np = 0; np < kSlots / 16; ++np) {
+                const int key = np * 16 + lm_row + ((lm_mat >> 1) << 3);
+                const int dim = kk * 16 + ((lm_mat & 1) << 3);
+                uint32_t b0, b1, b2, b3;
+                ldmatrix_x4(smem_u32(sk + key * S::kRow + dim), b0, b1, b2, b3);
+                Half<T>::mma(s[2 * np], qf[kk], b0, b1);
+                Half<T>::mma(s[2 * np + 1], qf[kk], b2, b3);
+            }
+        }
+
+        // Scores in base 2.  Column of s[n][c]: 8n + 2t + (c & 1); row: c >> 1.
+        if (cap) {
+#pragma unroll
+            for (int n = 0; n < kSlots / 8; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[n][c] = p.s2 * tanhf(s[n][c] * p.s1);
+        } else {
+#pragma unroll
+            for (int n = 0; n < kSlots / 8; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[n][c] *= p.s1;
+        }
+        if (bias || !full) {
+#pragma unroll
+            for (int n = 0; n < kSlots / 8; ++n) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int2 key = meta[n * 8 + 2 * t + (c & 1)];
+                    const int pos = c < 2 ? pos0 : pos1;
+                    float x = s[n][c];
+                    if (bias) x -= slope * (float)(abs(pos - key.x) - (c < 2 ? near0 : near1));
+                    if (!full) {
+                        bool see = key.x >= 0 && in_sight(p, u.prefix, pos, key.x);
+                        if (docs) see = see && key.y >= 0 && key.y == (c < 2 ? doc0 : doc1);
+                        if (!see) x = -INFINITY;
+                    }
+                    s[n][c] = x;
+                }
+            }
+        }
+
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kSlots / 8; ++n) {
+            mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
+            mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
+        }
+        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 1));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 2));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 1));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 2));
+        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+        const float base0 = mn0 == -INFINITY ? 0.f : mn0;
+        const float base1 = mn1 == -INFINITY ? 0.f : mn1;
+        const float corr0 = exp2f(m0 - base0), corr1 = exp2f(m1 - base1);
+        m0 = mn0;
+        m1 = mn1;
+        float ls0 = 0.f, ls1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < kSlots / 8; ++n) {
+            s[n][0] = exp2f(s[n][0] - base0);
+            s[n][1] = exp2f(s[n][1] - base0);
+            s[n][2] = exp2f(s[n][2] - base1);
+            s[n][3] = exp2f(s[n][3] - base1);
+            ls0 += s[n][0] + s[n][1];
+            ls1 += s[n][2] + s[n][3];
+        }
+        l0 = l0 * corr0 + ls0;
+        l1 = l1 * corr1 + ls1;
+#pragma unroll
+        for (int nd = 0; nd < DH / 8; ++nd) {
+            o[nd][0] *= corr0;
+            o[nd][1] *= corr0;
+            o[nd][2] *= corr1;
+            o[nd][3] *= corr1;
+        }
+#pragma unroll
+        for (int kk = 0; kk < kSlots / 16; ++kk) {
+            const uint32_t pa[4] = {Half<T>::pack(s[2 * kk][0], s[2 * kk][1]), Half<T>::pack(s[2 * kk][2], s[2 * kk][3]),
+                                    Half<T>::pack(s[2 * kk + 1][0], s[2 * kk + 1][1]),
+                                    Half<T>::pack(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+#pragma unroll
+            for (int dp = 0; dp < DH / 16; ++dp) {
+                const int key = kk * 16 + lm_row + ((lm_mat & 1) << 3);
+                const int dim = dp * 16 + ((lm_mat >> 1) << 3);
+                uint32_t b0, b1, b2, b3;
+                ldmatrix_x4_trans(smem_u32(sv + key * S::kRow + dim), b0, b1, b2, b3);
+                Half<T>::mma(o[2 * dp], pa, b0, b1);
+                Half<T>::mma(o[2 * dp + 1], pa, b2, b3);
+            }
+        }
+        __syncthreads();   // every warp is done with this stage before it is refilled
+    }
+
+    l0 += __shfl_xor_sync(kFull, l0, 1);
+    l0 += __shfl_xor_sync(kFull, l0, 2);
+    l1 += __shfl_xor_sync(kFull, l1, 1);
+    l1 += __shfl_xor_sync(kFull, l1, 2);
+    const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
+    bool bad0 = false, bad1 = false;
+#pragma unroll
+    for (int nd = 0; nd < DH / 8; ++nd) {
+        bad0 = bad0 || !isfinite(o[nd][0]) || !isfinite(o[nd][1]);
+        bad1 = bad1 || !isfinite(o[nd][2]) || !isfinite(o[nd][3]);
+    }
+    // a row that saw nothing is zero whatever its accumulators hold
+    T *out = static_cast<T *>(p.a.out) + u.b * p.c.out_stride[0] + head * p.c.out_stride[1];
+    uint32_t *o0 = reinterpret_cast<uint32_t *>(out + token * p.c.out_stride[2]);
+    uint32_t *o1 = reinterpret_cast<uint32_t *>(out + (token + 8) * p.c.out_stride[2]);
+#pragma unroll
+    for (int nd = 0; nd < DH / 8; ++nd) {
+        if (ok0) o0[nd * 4 + t] = l0 == 0.f ? 0u : Half<T>::pack(o[nd][0] * inv0, o[nd][1] * inv0);
+        if (ok1) o1[nd * 4 + t] = l1 == 0.f ? 0u : Half<T>::pack(o[nd][2] * inv1, o[nd][3] * inv1);
+    }
+    if (p.a.lse && t == 0) {
+        float *lse = p.a.lse + ((size_t)u.b * p.c.q_heads + head) * p.c.nq_tokens + token;
+        const float unit = bias ? p.a.slopes[head] : 0.f;
+        if (ok0) lse[0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * kLn2 - unit * (float)near0;
+        if (ok1) lse[8] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * kLn2 - unit * (float)near1;
+    }
+    // rows to compute on their own, one bit for each of the warp's 16
+    const unsigned b0 = __ballot_sync(kFull, bad0 && ok0 && l0 != 0.f);
+    const unsigned b1 = __ballot_sync(kFull, bad1 && ok1 && l1 != 0.f);
+    for (int r = 0; r < 16 && (b0 | b1); ++r) {
+        if (!(((r < 8 ? b0 : b1) >> (4 * (r & 7))) & 15u)) continue;
+        const int near = __shfl_sync(kFull, r < 8 ? near0 : near1, 4 * (r & 7));
+        row_alone<T, DH>(p, u, s_list, n_list, row0 + r, near);
+    }
+}
+
+template <typename T, int DH>
+cudaError_t launch(const Masked &p, unsigned units, cudaStream_t s) {
+    using S = Shape<DH>;
+    auto kern = masked_attention_kernel<T, DH>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    const int warps = min(kMaxWarps, (p.group << p.shift) / 16);
+    kern<<<units * (unsigned)p.tiles, 32 * warps, S::kSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+bool soft_cap_ok(float x) { return x == 0.f || (x >= 1e-3f && x <= 1e30f); }
+
+bool strides_ok(const int64_t (&s)[3]) {
+    for (int64_t x : s)
+        if (x < 0 || x % 8 != 0 || x > (1ll << 40)) return false;
+    return true;
+}
+
+bool config_ok(const rr_masked_attn_config *c) {
+    if (!c) return false;
+    if (c->batch < 0 || c->nq_tokens < 0 || c->nk_tokens < 0 || c->q_offset < 0) return false;
+    if (c->kv_heads < 1 || c->route_heads < 1 || c->q_heads < 1) return false;
+    if (c->route_heads % c->kv_heads != 0 || c->q_heads % c->route_heads != 0) return false;
+    if (c->dh != 64 && c->dh != 128) return false;
+    if (c->chunk != 16 && c->chunk != 32 && c->chunk != 64 && c->chunk != 128) return false;
+    if (c->width < 0 || c->width > kMaxWidth || c->route_stride < (c->width > 1 ? c->width : 1)) return false;
+    if (c->dtype != RR_BF16 && c->dtype != RR_F16) return false;
+    if ((long long)c->q_offset + c->nq_tokens > 1 << 24 || c->nk_tokens > 1 << 24) return false;
+    if (!(c->scale >= 0.f) || !isfinite(c->scale)) return false;
+    if (!(c->scale <= 1e30f) || !soft_cap_ok(c->soft_cap)) return false;
+    if (!strides_ok(c->q_stride) || !strides_ok(c->k_stride) || !strides_ok(c->v_stride) || !strides_ok(c->out_stride))
+        return false;
+    const int out_sizes[3] = {c->batch, c->q_heads, c->nq_tokens};
+    for (int i = 0; i < 3; ++i)
+        if (out_sizes[i] > 1 && c->out_stride[i] == 0) return false;
+    const long long group = c->q_heads / c->route_heads, chunks = (c->nq_tokens + c->chunk - 1) / c->chunk;
+    const long long heads = (long long)c->batch * c->route_heads, rows16 = group * c->chunk / 16;
+    if (chunks > 0 && heads > 0x7fffffffLL / chunks) return false;
+    if (heads * chunks > 0 && rows16 > 0x7fffffffLL / (heads * chunks)) return false;
+    return true;
+}
+
+}  // namespace rr_masked
+
+extern "C" rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const rr_masked_attn_args *args,
+                                         void *stream) {
+    using namespace rr_masked;
+    if (!config_ok(cfg) || !args) return RR_EINVAL;
+    if (cfg->batch == 0 || cfg->nq_tokens == 0) return RR_OK;
+    const rr_masked_attn_args &a = *args;
+    if (!a.q || !a.out || !aligned(a.q, 16) || !aligned(a.out, 16)) return RR_EINVAL;
+    if (cfg->width > 0 && (!a.route || !aligned(a.route, 4))) return RR_EINVAL;
+    if (cfg->nk_tokens > 0 && (!a.k || !a.v || !aligned(a.k, 16) || !aligned(a.v, 16))) return RR_EINVAL;
+    if (cfg->nk_tokens > 0 ? !a.doc_q != !a.doc_k : a.doc_k && !a.doc_q) return RR_EINVAL;
+    if (!aligned(a.slopes, 4) || !aligned(a.doc_q, 4) || !aligned(a.doc_k, 4) || !aligned(a.prefix, 4) ||
+        !aligned(a.lse, 4))
+        return RR_EINVAL;
+    Masked p;
+    p.c = *cfg;
+    p.a = a;
+    p.group = cfg->q_heads / cfg->route_heads;
+    p.shift = cfg->chunk == 16 ? 4 : cfg->chunk == 32 ? 5 : cfg->chunk == 64 ? 6 : 7;
+    p.nqc = (cfg->nq_tokens + cfg->chunk - 1) >> p.shift;
+    p.nkc = (cfg->nk_tokens + cfg->chunk - 1) >> p.shift;
+    const float scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->dh);
+    p.s1 = cfg->soft_cap > 0.f ? scale / cfg->soft_cap : scale * kLog2e;
+    p.s2 = cfg->soft_cap * kLog2e;
+    p.tiles = ((p.group << p.shift) + 16 * kMaxWarps - 1) / (16 * kMaxWarps);
+    const unsigned units = (unsigned)((long long)cfg->batch * cfg->route_heads * p.nqc);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (cfg->dtype == RR_BF16)
+        e = cfg->dh == 64 ? launch<__nv_bfloat16, 64>(p, units, s) : launch<__nv_bfloat16, 128>(p, units, s);
+    else
+        e = cfg->dh == 64 ? launch<__half, 64>(p, units, s) : launch<__half, 128>(p, units, s);
+    return e == cudaSuccess ? RR_OK : RR_ECUDA;
+}

@@ -1,0 +1,211 @@
+// rr_masked.cuh -- what the kernels of the masked attention share (declared in
+// include/rr_attention.h): the problem, the list of a unit's key chunks, the
+// masks, and the row that is computed on its own.
+//
+// A unit is one query chunk of one route head: the `group` query heads that
+// share the route (and therefore the key head) times the chunk's tokens, rows
+// numbered head * chunk + token.  All of its rows read the same key chunks.
+#pragma once
+
+#include <limits.h>
+#include <math.h>
+
+#include "../../include/rr_attention.h"
+#include "rr_frag.cuh"
+
+namespace rr_masked {
+
+using rr_attn::Half;
+using rr_attn::kFull;
+using rr_attn::kMaxWidth;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kChunkFull = 1 << 30;   // list flag: every key of the chunk is visible to every row
+constexpr int kChunkId = kChunkFull - 1;
+
+struct Masked {
+    rr_masked_attn_config c;
+    rr_masked_attn_args a;
+    int group;        // query heads per route head
+    int shift;        // log2(chunk)
+    int nqc, nkc;     // query and key chunks
+    int tiles;        // row tiles per unit
+    // scores in base 2: x log2(e) = s * s1 without a cap, s2 * tanh(s * s1) with one
+    float s1, s2;
+};
+
+struct Unit {
+    int b, route_head, i, tile;   // batch entry, route head, query chunk, row tile
+    int kv_head;
+    int tokens;                   // valid query tokens of the chunk
+    int p_first, p_last;          // positions of its first and last valid token
+    int prefix;                   // keys below it are visible under causal
+};
+
+__device__ __forceinline__ Unit unit_of(const Masked &p, unsigned block) {
+    Unit u;
+    u.tile = (int)(block % (unsigned)p.tiles);
+    unsigned r = block / (unsigned)p.tiles;
+    u.i = (int)(r % (unsigned)p.nqc);
+    r /= (unsigned)p.nqc;
+    u.route_head = (int)(r % (unsigned)p.c.route_heads);
+    u.b = (int)(r / (unsigned)p.c.route_heads);
+    u.kv_head = u.route_head / (p.c.route_heads / p.c.kv_heads);
+    u.tokens = min(p.c.chunk, p.c.nq_tokens - (u.i << p.shift));
+    u.p_first = p.c.q_offset + (u.i << p.shift);
+    u.p_last = u.p_first + u.tokens - 1;
+    u.prefix = p.a.prefix ? p.a.prefix[u.b] : 0;
+    return u;
+}
+
+// Smallest and largest of n int32 at x, by a warp.
+__device__ __forceinline__ void warp_min_max(const int32_t *x, int n, int &lo, int &hi) {
+    lo = INT_MAX;
+    hi = INT_MIN;
+    for (int e = threadIdx.x & 31; e < n; e += 32) {
+        const int v = x[e];
+        lo = min(lo, v);
+        hi = max(hi, v);
+    }
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+}
+
+// The unit's route in shared memory: list[0..n-1] = key chunks that can hold a
+// visible key, in route order, kChunkFull set where all of their keys are
+// visible to all rows (neither the masks nor the last chunk's end cut them).
+// By the whole block; ends with a barrier.
+__device__ __forceinline__ int build_list(const Masked &p, const Unit &u, int32_t *list, int32_t *n_out) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int32_t *route =
+        p.a.route + (((size_t)u.b * p.c.route_heads + u.route_head) * p.nqc + u.i) * (size_t)p.c.route_stride;
+    const int width = p.c.width;
+    const bool causal = p.c.causal != 0, docs = p.a.doc_q != nullptr;
+    for (int e = threadIdx.x; e < width; e += blockDim.x) {
+        int j = route[e];
+        if (j < 0 || j >= p.nkc) j = -1;
+        if (j >= 0) {
+            const int lo = j << p.shift, hi = min(lo + p.c.chunk, p.c.nk_tokens);
+            bool full = hi - lo == p.c.chunk;
+            if (causal) {
+                if (lo > u.p_last && lo >= u.prefix) j = -1;
+                full = full && (hi - 1 <= u.p_first || hi <= u.prefix);
+            }
+            if (j >= 0 && full) j |= kChunkFull;
+        }
+        list[e] = j;
+    }
+    __syncthreads();
+    if (docs) {
+        // documents are mostly runs of tokens: a chunk of one document is either
+        // visible to a query chunk of one document as a whole or not at all
+        int qlo, qhi;
+        warp_min_max(p.a.doc_q + (size_t)u.b * p.c.nq_tokens + (u.i << p.shift), u.tokens, qlo, qhi);
+        for (int e = warp; e < width; e += warps) {
+            const int j = list[e];
+            if (j < 0) continue;
+            const int lo = (j & kChunkId) << p.shift;
+            int klo, khi;
+            warp_min_max(p.a.doc_k + (size_t)u.b * p.c.nk_tokens + lo, min(p.c.chunk, p.c.nk_tokens - lo), klo, khi);
+            if (lane == 0) {
+                if (khi < 0 || qhi < 0 || khi < qlo || klo > qhi) list[e] = -1;
+                else if (klo != khi || qlo != qhi) list[e] = j & ~kChunkFull;
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        int n = 0;
+        for (int e0 = 0; e0 < width; e0 += 32) {
+            const int j = e0 + lane < width ? list[e0 + lane] : -1;
+            const unsigned m = __ballot_sync(kFull, j >= 0);
+            __syncwarp();
+            if (j >= 0) list[n + __popc(m & ((1u << lane) - 1u))] = j;
+            n += __popc(m);
+            __syncwarp();
+        }
+        if (lane == 0) *n_out = n;
+    }
+    __syncthreads();
+    return *n_out;
+}
+
+// Key s against a query at position pos: the causal rule with its exception.
+__device__ __forceinline__ bool in_sight(const Masked &p, int prefix, int pos, int s) {
+    return p.c.causal == 0 || s <= pos || s < prefix;
+}
+
+// Distance from a row to the nearest key that it sees, among list entries
+// first, first + step, ... (INT_MAX: none).  The bias is taken relative to it,
+// so that a row whose keys are all far away keeps the bits of its scores: at
+// distance 2^20 a product slope * distance in fp32 has a step of 1/16.
+__device__ __forceinline__ int nearest(const Masked &p, const Unit &u, const int32_t *list, int n, int pos, int doc,
+                                       int first, int step) {
+    int best = INT_MAX;
+    for (int e = first; e < n; e += step) {
+        const int lo = (list[e] & kChunkId) << p.shift;
+        int hi = min(lo + p.c.chunk, p.c.nk_tokens);
+        if (p.c.causal) hi = min(hi, max(pos + 1, u.prefix));
+        if (hi <= lo) continue;
+        const int d = pos < lo ? lo - pos : pos >= hi ? pos - (hi - 1) : 0;
+        if (d >= best) continue;
+        if (!p.a.doc_q || (list[e] & kChunkFull)) {
+            best = d;
+        } else {
+            const int32_t *dk = p.a.doc_k + (size_t)u.b * p.c.nk_tokens;
+            for (int s = lo; s < hi; ++s)
+                if (dk[s] == doc) best = min(best, abs(pos - s));
+        }
+    }
+    return best;
+}
+
+// One row computed by a warp, key by key, reading only what it sees: the way
+// out for a row whose accumulators hold an infinity or a NaN.  There a masked
+// value row that holds one has met a weight of zero in the matrix product, or
+// the row's own result is not finite; both end here with the right values.
+// `row` numbers the unit's rows.
+template <typename T, int DH>
+__device__ __noinline__ void row_alone(const Masked &p, const Unit &u, const int32_t *list, int n, int row, int near) {
+    constexpr int E = DH / 32;
+    const int lane = threadIdx.x & 31;
+    const int head = u.route_head * p.group + (row >> p.shift), token = (u.i << p.shift) + (row & (p.c.chunk - 1));
+    const int pos = p.c.q_offset + token;
+    const T *q = static_cast<const T *>(p.a.q) + u.b * p.c.q_stride[0] + head * p.c.q_stride[1] +
+                 token * p.c.q_stride[2] + lane * E;
+    const T *k = static_cast<const T *>(p.a.k) + u.b * p.c.k_stride[0] + u.kv_head * p.c.k_stride[1] + lane * E;
+    const T *v = static_cast<const T *>(p.a.v) + u.b * p.c.v_stride[0] + u.kv_head * p.c.v_stride[1] + lane * E;
+    const int doc = p.a.doc_q ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + token] : 0;
+    const float slope = p.a.slopes ? p.a.slopes[head] * kLog2e : 0.f;
+    float qf[E], o[E];
+    for (int e = 0; e < E; ++e) {
+        qf[e] = Half<T>::up(q[e]);
+        o[e] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;
+    for (int it = 0; it < n; ++it) {
+        const int lo = (list[it] & kChunkId) << p.shift, hi = min(lo + p.c.chunk, p.c.nk_tokens);
+        for (int s = lo; s < hi; ++s) {
+            if (!in_sight(p, u.prefix, pos, s)) continue;
+            if (p.a.doc_q && (doc < 0 || p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] != doc)) continue;
+            float x = 0.f;
+            for (int e = 0; e < E; ++e) x += qf[e] * Half<T>::up(k[s * p.c.k_stride[2] + e]);
+            for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
+            x *= p.s1;
+            if (p.c.soft_cap > 0.f) x = p.s2 * tanhf(x);
+            if (p.a.slopes) x -= slope * (float)(abs(pos - s) - near);
+            const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.f : mn;
+            const float corr = exp2f(m - base), w = exp2f(x - base);
+            m = mn;
+            l = l * corr + w;
+            for (int e = 0; e < E; ++e)
+                o[e] = o[e] * corr + w * Half<T>::up(v[s * p.c.v_stride[2] + e]);
+        }
+    }
+    T *out = static_cast<T *>(p.a.out) + u.b * p.c.out_stride[0] + head * p.c.out_stride[1] +
+             token * p.c.out_stride[2] + lane * E;
+    for (int e = 0; e < E; ++e) out[e] = Half<T>::down(l == 0.f ? 0.f : o[e] / l);
+}
+
+}  // namespace rr_masked

@@ -56,7 +56,11 @@ typedef enum {
     RR_ECAPACITY = 6 /* the problem exceeds a fixed capacity (rr_route_layer_static) */
 } rr_status;
 
-typedef enum { RR_F32 = 0, RR_BF16 = 1 } rr_dtype;
+typedef enum {
+    RR_F32 = 0,
+    RR_BF16 = 1,
+    RR_F16 = 2   /* the operators of rr_attention.h and rr_cache.h that say so; never a ledger */
+} rr_dtype;
 
 /* Problem statement of one ledger (RouteRelay §2.1, §3.1, §3.2, Table 1).
  * Limits: 1 <= k <= nk; k + m_near <= 128; r_rand <= 128; d a multiple of 8

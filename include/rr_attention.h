@@ -71,6 +71,75 @@ rr_status rr_sparse_attention(const rr_attn_config *cfg, const void *d_q, const 
                               const void *d_v, const int32_t *d_route, float *d_out,
                               void *stream);
 
+/* ---- masked attention over a route ---------------------------------------
+ * The attention above with the score terms and masks of a prompt:
+ *
+ *   x(t, s) = cap * tanh(scale * q_t . k_s / cap)        (cap > 0; else the product)
+ *             - slope_h * |p_t - s|,                      p_t = t + q_offset
+ *   s is visible to t iff s belongs to a chunk of the route of t's query chunk,
+ *     causal == 0, or s <= p_t, or s < prefix_b, and
+ *     doc_q(t) == doc_k(s) >= 0 where documents are given;
+ *   o_t = sum_s e^x(t,s) v_s / sum_s e^x(t,s),   lse_t = log sum_s e^x(t,s)
+ *
+ * over the visible s, an entry that the route repeats counting once per
+ * occurrence.  A token with no visible key gets a zero row and lse -inf.
+ * Query chunk i holds query tokens i*chunk .. i*chunk + chunk - 1 (positions
+ * q_offset later), key chunk j key tokens j*chunk ..; the last chunk of either
+ * may be short.  Key/value heads and routes may be shared: query head h uses
+ * route head h / (q_heads / route_heads) and key head h / (q_heads / kv_heads).
+ * What a masked key or value row holds is never read into a result, infinities
+ * and NaN included. */
+
+/* Limits: batch, nq_tokens, nk_tokens >= 0; kv_heads divides route_heads
+ * divides q_heads; dh in {64, 128}; chunk in {16, 32, 64, 128}; 0 <= width <=
+ * 1024; route_stride >= max(width, 1); dtype RR_BF16 or RR_F16; q_offset >= 0
+ * and q_offset + nq_tokens, nk_tokens <= 2^24 (positions are exact in fp32);
+ * scale >= 0 and at most 1e30; soft_cap 0 or in [1e-3, 1e30]; batch * route_heads * query chunks *
+ * ceil(q_heads / route_heads * chunk / 16) <= 2^31 - 1; strides in
+ * elements, >= 0 and multiples of 8 (those of `out` of a size above 1, > 0). */
+typedef struct {
+    int32_t batch;
+    int32_t q_heads;      /* query (and output) heads */
+    int32_t kv_heads;     /* key / value heads */
+    int32_t route_heads;  /* routes per batch entry */
+    int32_t nq_tokens;    /* query tokens */
+    int32_t nk_tokens;    /* key / value tokens */
+    int32_t dh;           /* head dimension */
+    int32_t chunk;        /* tokens per chunk */
+    int32_t width;        /* route entries read per query chunk */
+    int32_t route_stride; /* int32 elements from one query chunk's route to the next */
+    int32_t causal;       /* nonzero: causal mask, with the prefix's exception */
+    int32_t dtype;        /* rr_dtype of q, k, v and out */
+    int32_t q_offset;     /* position of query token 0 */
+    float scale;          /* 0 selects 1/sqrt(dh) */
+    float soft_cap;       /* 0: no cap */
+    int64_t q_stride[3];  /* elements from one batch entry, head, token to the next */
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int64_t out_stride[3];
+} rr_masked_attn_config;
+
+/* Device pointers of one call; those marked optional may be NULL. */
+typedef struct {
+    const void *q;           /* [batch, q_heads, nq_tokens, dh] by q_stride; 16-byte aligned */
+    const void *k;           /* [batch, kv_heads, nk_tokens, dh] by k_stride; 16-byte aligned */
+    const void *v;           /* the same by v_stride */
+    const int32_t *route;    /* [batch, route_heads, ceil(nq_tokens / chunk), route_stride] */
+    const float *slopes;     /* optional [q_heads]: bias by distance, finite and >= 0 */
+    const int32_t *doc_q;    /* optional [batch, nq_tokens]: document of each query token */
+    const int32_t *doc_k;    /* [batch, nk_tokens], given iff doc_q is */
+    const int32_t *prefix;   /* optional [batch]: keys below it are visible under causal */
+    void *out;               /* [batch, q_heads, nq_tokens, dh] by out_stride; 16-byte aligned */
+    float *lse;              /* optional [batch, q_heads, nq_tokens] */
+} rr_masked_attn_args;
+
+/* Enqueues the attention.  Scores, softmax and sums are fp32; the weights are
+ * rounded to the inputs' type for the product with v, and the result to that
+ * type once.  Errors: RR_EINVAL (shape, stride, null or
+ * misaligned pointer), RR_ECUDA (launch). */
+rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const rr_masked_attn_args *args,
+                              void *stream);
+
 #ifdef __cplusplus
 }
 #endif
