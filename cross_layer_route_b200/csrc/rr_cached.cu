@@ -13,8 +13,9 @@
 //   O^T = V^T P^T A = 16 dims x 16 tokens.  A lane holds 4 tokens' bytes of the
 //                 same dims; bytes of two tokens are paired with prmt.
 // Codes become f16 exactly.  The scales are powers of two: a row's goes to its
-// score (keys) or its weight (values); with one for every 32 elements a code is
-// multiplied by its group's scale over the row's largest, exact down to 2^-35.
+// score (keys) or its weight (values).  With one for every 32 elements, a key's
+// groups are summed one by one in fp32, and a value's codes are multiplied by
+// their group's scale over the row's largest, exact down to 2^-35.
 // Weights are f16 and relative to the largest weight * scale seen so far, which
 // stands at 2^7 (and at 2^15 before it is noticed), so neither a wide spread of
 // scales nor a long tail of small weights is lost; the sum of the weights is
@@ -22,7 +23,7 @@
 // of the scores: a score of 2^24 or more would swallow a scale added to it.
 // The references move only when a score passes them by 2^8: most steps then
 // cost one vote and no shuffles.
-// The loop is bound by HBM: a step's bytes are loaded one step ahead.
+// A warp copies its steps (cp.async) into a ring of its own, two or three ahead.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -37,11 +38,15 @@ using namespace rr_attn;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kAttnWarps = 8;
+constexpr int kAttnWarps = 6;
+constexpr int kJoinWarps = 4;
 constexpr float kLift = 7.f;     // weights are 2^7 at the maximum
 constexpr float kSlack = 8.f;    // ... and 2^15 at most
 constexpr int kGroupLift = 12;   // codes of 4 bits carry 2^12
 constexpr int kState = 4;        // floats beside a partial row: max, sum, value reference, nearest
+
+// CTAs per SM: what 128 O values a thread and the other fragments leave room for.
+constexpr int ctas_per_sm(int dh, int nt) { return nt * dh <= 128 ? 2 : 1; }
 
 struct Cached {
     rr_cache_config c;
@@ -61,83 +66,131 @@ struct Words {
     static constexpr int kV = FMT == RR_E4M3 ? DH / 32 : DH / 64;
     static constexpr int kRowBytes = FMT == RR_E4M3 ? DH : DH / 2;
     static constexpr int kGroups = FMT == RR_E4M3 ? 1 : DH / 32;
+    // A step (16 tokens of a page) in shared memory: keys, values, their scales.
+    static constexpr int kSide = 16 * kRowBytes;
+    static constexpr int kScales = 16 * kGroups;
+    static constexpr int kStage = 2 * kSide + 2 * kScales;
+    // pairs of steps that a warp's ring holds, one of them in use: twelve warps on
+    // an SM then have 100 KB of copies in flight
+    static constexpr int kPairs = kRowBytes == 128 ? 2 : 3;
+    static constexpr int kRing = kPairs * 2 * kStage;
 };
 
-// One step's bytes: 16 tokens of a page.
+// Byte offset of 16-byte piece `c` of row `r` in a step's keys or values.  Rows
+// lie in lines of 128 bytes, whose eight pieces are permuted so that the lanes
+// that read together meet eight different pieces: a key row's pieces by the
+// lanes of a token or (one piece of each group of 32 elements) by all tokens, a
+// value row's by the lanes of a dim range for tokens 2t.
+template <int ROW, bool VALUES>
+__device__ __forceinline__ int piece_at(int r, int c) {
+    constexpr int kPer = 128 / ROW;                  // rows per line
+    const int line = r / kPer, at = (r % kPer) * (ROW / 16) + c;
+    const int turn = VALUES ? 2 * ((ROW == 128 ? line >> 1 : line) & 3) : ROW == 128 ? 4 * (line & 1) : line & 3;
+    return line * 128 + ((at ^ turn) << 4);
+}
+
+// Starts the copy of one step: 16 tokens from row `krow` of the pool on.  Values
+// behind the sequence's end are whatever the page held, and a NaN code there
+// would meet a weight of zero in the product: zeros in their place.  pos < 0:
+// all zeros.  `kat`, `vat`: this lane's first pieces.
 template <int FMT, int DH>
-struct Step {
-    uint32_t k[2][Words<FMT, DH>::kK];   // tokens g, g + 8
-    uint32_t v[4][Words<FMT, DH>::kV];   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-    uint32_t ks[2], vs[2];               // scale bytes of tokens g, g + 8
-    int pos;                             // position of token 0; < 0: skipped
-};
+__device__ __forceinline__ void copy_step(uint32_t stage, uint32_t kat, uint32_t vat, const Cached &p, size_t krow,
+                                          int pos, int len) {
+    using W = Words<FMT, DH>;
+    constexpr int kPieces = W::kSide / 16, kCopies = (kPieces + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    const unsigned char *codes = static_cast<const unsigned char *>(p.pool.codes) + krow * W::kRowBytes + 16 * lane;
+    const unsigned char *values = codes + p.c.chunk * W::kRowBytes;
+    const int side = lane / W::kGroups, c = lane % W::kGroups;
+    const unsigned char *scales =
+        static_cast<const unsigned char *>(p.pool.scales) + (krow + side * p.c.chunk) * W::kGroups + 16 * c;
+    const uint32_t sat = stage + 2 * W::kSide + side * W::kScales + 16 * c;
+    // piece lane + 32 i lies 512 i behind the lane's first; the values' pieces of
+    // rows of 128 bytes change places every four rows
+    const uint32_t vodd = W::kRowBytes == 128 ? vat ^ 64 : vat;
+    if (pos >= 0 && pos + 16 <= len) {
+        if (kPieces >= 32 || lane < kPieces) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                cp_async16(stage + kat + 512 * i, codes + 512 * i);
+                cp_async16(stage + W::kSide + (i & 1 ? vodd : vat) + 512 * i, values + 512 * i);
+            }
+        }
+        if (lane < 2 * W::kGroups) cp_async16(sat, scales);
+    } else {
+        const int left = pos < 0 ? 0 : len - pos;
+        if (kPieces >= 32 || lane < kPieces) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int r = (lane + 32 * i) / (W::kRowBytes / 16);
+                cp_async16_zfill(stage + kat + 512 * i, codes + 512 * i, left ? 16 : 0);
+                cp_async16_zfill(stage + W::kSide + (i & 1 ? vodd : vat) + 512 * i, values + 512 * i, r < left ? 16 : 0);
+            }
+        }
+        if (lane < 2 * W::kGroups) cp_async16_zfill(sat, scales, left ? 16 : 0);
+    }
+}
 
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const unsigned char *x) {
+__device__ __forceinline__ void read_words(uint32_t (&w)[N], const unsigned char *x) {
     if constexpr (N == 4) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
+        const uint4 a = *reinterpret_cast<const uint4 *>(x);
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     } else if constexpr (N == 2) {
-        const uint2 a = __ldg(reinterpret_cast<const uint2 *>(x));
+        const uint2 a = *reinterpret_cast<const uint2 *>(x);
         w[0] = a.x, w[1] = a.y;
     } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(x));
+        w[0] = *reinterpret_cast<const uint32_t *>(x);
     }
 }
 
+// Key words of token r, lane quarter t: of the 16-byte pieces t and t + 4, or of
+// piece t; with a scale for every 32 elements word t of each group's piece, so
+// that one k-step stays within one group.
 template <int FMT, int DH>
-__device__ __forceinline__ uint32_t load_scales(const unsigned char *scales, size_t row) {
-    if constexpr (FMT == RR_E4M3) return __ldg(scales + row);
-    else if constexpr (DH == 64) return __ldg(reinterpret_cast<const uint16_t *>(scales) + row);
-    else return __ldg(reinterpret_cast<const uint32_t *>(scales) + row);
-}
-
-template <int FMT, int DH>
-__device__ __forceinline__ void load_step(Step<FMT, DH> &s, const Cached &p, int head, int page, int pos, int len) {
+__device__ __forceinline__ void read_key(uint32_t (&w)[Words<FMT, DH>::kK], const unsigned char *stage, int r, int t) {
     using W = Words<FMT, DH>;
-    s.pos = pos;
-    if (pos < 0) return;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int place = pos & (p.c.chunk - 1);
-    const size_t krow = ((size_t)page * p.c.heads + head) * 2 * p.c.chunk + place, vrow = krow + p.c.chunk;
-    const unsigned char *codes = static_cast<const unsigned char *>(p.pool.codes);
-    const unsigned char *scales = static_cast<const unsigned char *>(p.pool.scales);
+    if constexpr (FMT == RR_E2M1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const unsigned char *x = codes + (krow + g + 8 * i) * W::kRowBytes;
-        if constexpr (W::kK == 8) {
-            uint32_t a[4], b[4];
-            load_words(a, x + 16 * t);
-            load_words(b, x + 64 + 16 * t);
+        for (int j = 0; j < W::kGroups; ++j)
+            w[j] = *reinterpret_cast<const uint32_t *>(stage + piece_at<W::kRowBytes, false>(r, j) + 4 * t);
+    } else {
+        uint32_t a[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s.k[i][j] = a[j], s.k[i][4 + j] = b[j];
-        } else {
-            load_words(s.k[i], x + 4 * W::kK * t);
-        }
-        s.ks[i] = load_scales<FMT, DH>(scales, krow + g + 8 * i);
-        s.vs[i] = load_scales<FMT, DH>(scales, vrow + g + 8 * i);
-    }
-    // values behind the sequence's end are whatever the page held: a NaN code
-    // there would meet a weight of zero in the product
+        for (int h = 0; h < W::kK / 4; ++h) {
+            read_words(a, stage + piece_at<W::kRowBytes, false>(r, t + 4 * h));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
-        if (pos + tok < len) {
-            load_words(s.v[i], codes + (vrow + tok) * W::kRowBytes + 4 * W::kV * g);
-        } else {
-#pragma unroll
-            for (int j = 0; j < W::kV; ++j) s.v[i][j] = 0u;
+            for (int j = 0; j < 4; ++j) w[4 * h + j] = a[j];
         }
     }
 }
 
+template <int FMT, int DH>
+__device__ __forceinline__ void read_value(uint32_t (&w)[Words<FMT, DH>::kV], const unsigned char *stage, int r, int g) {
+    using W = Words<FMT, DH>;
+    const int at = 4 * W::kV * g;
+    read_words(w, stage + W::kSide + piece_at<W::kRowBytes, true>(r, at / 16) + at % 16);
+}
+
+template <int FMT, int DH>
+__device__ __forceinline__ uint32_t read_scales(const unsigned char *stage, int side, int r) {
+    using W = Words<FMT, DH>;
+    const unsigned char *x = stage + 2 * W::kSide + side * W::kScales + r * W::kGroups;
+    if constexpr (W::kGroups == 1) return *x;
+    else if constexpr (W::kGroups == 2) return *reinterpret_cast<const uint16_t *>(x);
+    else return *reinterpret_cast<const uint32_t *>(x);
+}
+
+// Two codes (the low 16 or 8 bits) as f16.
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+    uint32_t d;
+    asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(d) : "r"(two));
+    return d;
 }
 __device__ __forceinline__ uint32_t f16x2_of_e2m1(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)two, __NV_E2M1);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+    uint32_t d;
+    asm("{.reg .b8 x, y, z, w; mov.b32 {x, y, z, w}, %1; cvt.rn.f16x2.e2m1x2 %0, x;}" : "=r"(d) : "r"(two));
+    return d;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     const __half2 c = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
@@ -150,27 +203,27 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
     return d;
 }
 
-// Largest of a row's scale bytes that are not NaN (0 if all are).
+// Largest of a row's scale bytes, NaN (255) among them.
 template <int G>
-__device__ __forceinline__ int top_scale(uint32_t w) {
-    int m = 0;
+__device__ __forceinline__ unsigned top_scale(uint32_t w) {
+    if constexpr (G == 1) return w;
+    const unsigned m = __vmaxu2(w & 0x00ff00ffu, (w >> 8) & 0x00ff00ffu);
+    return G == 2 ? m & 0xffffu : max(m & 0xffffu, m >> 16);
+}
+// The same without the NaN bytes (0 if all are).
+template <int G>
+__device__ __forceinline__ unsigned top_number(uint32_t w) {
+    unsigned m = 0;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-        const int b = (w >> (8 * i)) & 255;
-        m = max(m, b == 255 ? 0 : b);
+        const unsigned b = (w >> (8 * i)) & 255;
+        m = max(m, b == 255 ? 0u : b);
     }
     return m;
 }
-template <int G>
-__device__ __forceinline__ bool has_nan(uint32_t w) {
-    bool y = false;
-#pragma unroll
-    for (int i = 0; i < G; ++i) y = y || ((w >> (8 * i)) & 255) == 255;
-    return y;
-}
 // 2^(byte - top + kGroupLift) in f16; zero below 2^-24 and for NaN bytes.
-__device__ __forceinline__ uint32_t group_factor(uint32_t byte, int top) {
-    const int e = (int)byte - top + kGroupLift;
+__device__ __forceinline__ uint32_t group_factor(unsigned byte, unsigned top) {
+    const int e = (int)byte - (int)top + kGroupLift;
     if (byte == 255 || e < -24) return 0;
     return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
 }
@@ -184,16 +237,18 @@ __device__ __forceinline__ int query_shift(unsigned amax_bits) {
 }
 
 template <int FMT, int DH, int NT>
-__global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_attention_kernel(const __grid_constant__ Cached p) {
+__global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_attention_kernel(const __grid_constant__ Cached p) {
     using W = Words<FMT, DH>;
     constexpr int kRows = 8 * NT, kQRow = DH + 4;      // padded query rows: lanes 8 banks apart
     constexpr int kMT = DH / 16;                       // 16-dim tiles of the values
     constexpr int kKeep = kMT * 4 * NT + 6 * NT;       // floats of a warp's state per lane
+    constexpr int kGap = 16;
     extern __shared__ __align__(16) unsigned char smem[];
     __half *s_q = reinterpret_cast<__half *>(smem);                                   // [kRows][kQRow]
     float *s_row = reinterpret_cast<float *>(smem + kRows * kQRow * 2);               // [kRows] score factor
     int *s_near = reinterpret_cast<int *>(s_row + kRows);
-    float *s_merge = reinterpret_cast<float *>(smem + kRows * kQRow * 2 + kRows * 4 + 16);
+    unsigned char *s_ring = smem + kRows * kQRow * 2 + kRows * 4 + kGap;    // [warps][stages][stage]
+    float *s_merge = reinterpret_cast<float *>(s_ring);                               // after the loop
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y % p.c.heads, b = blockIdx.y / p.c.heads, row0 = blockIdx.z * kRows;
@@ -204,6 +259,55 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_atten
     const int sub_shift = p.shift - 4;                 // steps per chunk
     const long long all = (long long)entries << sub_shift;
     const int begin = (int)(all * blockIdx.x / p.splits), end = (int)(all * (blockIdx.x + 1) / p.splits);
+
+    // A warp takes pairs of steps, begin + 2 warp on and every 2 kAttnWarps after
+    // that; lane i looks up the page of the i-th of 32 steps.
+    const int mine = begin + 2 * warp < end ? (end - begin - 2 * warp + 2 * kAttnWarps - 1) / (2 * kAttnWarps) : 0;
+    int pos_l = -1;
+    size_t row_l = 0;
+    const uint32_t ring = smem_u32(s_ring) + warp * W::kRing;
+    uint32_t fill = ring;                              // the pair filled next
+    const int first_row = lane / (W::kRowBytes / 16), first_piece = lane % (W::kRowBytes / 16);
+    const uint32_t kat = piece_at<W::kRowBytes, false>(first_row, first_piece);
+    const uint32_t vat = piece_at<W::kRowBytes, true>(first_row, first_piece);
+    int queue[W::kPairs][2];                           // positions of the steps in flight, oldest first
+    auto fetch = [&](int i) {
+        if (i < mine) {
+            if ((i & 15) == 0) {
+                pos_l = -1;
+                row_l = 0;
+                const int step = begin + 2 * (warp + (i + (lane >> 1)) * kAttnWarps) + (lane & 1);
+                if (step < end) {
+                    const int entry = step >> sub_shift;
+                    const int id = route ? route[entry] : entry;
+                    if (id >= 0 && id < p.n.table_width) {
+                        const int at = (id << p.shift) + ((step & ((1 << sub_shift) - 1)) << 4);
+                        const int page = at < len ? table[id] : -1;
+                        if (page >= 0 && page < p.c.pages) {
+                            pos_l = at;
+                            row_l = ((size_t)page * p.c.heads + head) * 2 * p.c.chunk + (at & (p.c.chunk - 1));
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int from = 2 * (i & 15) + u;
+                const int pos = __shfl_sync(kFull, pos_l, from);
+                const size_t row = __shfl_sync(kFull, row_l, from);
+                queue[W::kPairs - 1][u] = pos;
+                copy_step<FMT, DH>(fill + u * W::kStage, kat, vat, p, row, pos, len);
+            }
+            fill = fill == ring + W::kRing - 2 * W::kStage ? ring : fill + 2 * W::kStage;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < W::kPairs - 1; ++i) {
+        fetch(i);
+        queue[i][0] = queue[W::kPairs - 1][0];
+        queue[i][1] = queue[W::kPairs - 1][1];
+    }
 
     // queries
     for (int r = warp; r < kRows; r += kAttnWarps) {
@@ -225,7 +329,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_atten
         const int shift = query_shift(amax);
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) s_q[r * kQRow + lane + 32 * i] = __float2half_rn(ldexpf(x[i], shift));
-        if (lane == 0) s_row[r] = ldexpf(p.s1, -shift - (FMT == RR_E2M1 ? kGroupLift : 0));
+        if (lane == 0) s_row[r] = ldexpf(p.s1, -shift);
     }
     // The distance that the bias is taken relative to: the newest token's to the
     // nearest key that has a page (see `nearest` of the masked attention).
@@ -252,7 +356,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_atten
 
     uint32_t qf[NT <= 2 ? NT : 1][DH / 16][2];
     auto query = [&](int nt, int j, uint32_t &b0, uint32_t &b1) {
-        const int dim = FMT == RR_E2M1 ? (DH / 4) * t + 4 * j : 64 * (j / 4) + 16 * t + 4 * (j % 4);
+        const int dim = FMT == RR_E2M1 ? 32 * (j / 2) + 8 * t + 4 * (j % 2) : 64 * (j / 4) + 16 * t + 4 * (j % 4);
         const uint2 w = *reinterpret_cast<const uint2 *>(s_q + (nt * 8 + g) * kQRow + dim);
         b0 = w.x;
         b1 = w.y;
@@ -290,121 +394,187 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_atten
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m1[nt][0] = m1[nt][1] = m2[nt][0] = m2[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
-    // A warp's steps begin + warp, + kAttnWarps, ...; lane i looks up the page of the i-th of 32.
-    const int mine = begin + warp < end ? (end - begin - warp + kAttnWarps - 1) / kAttnWarps : 0;
-    int page_l = -1, pos_l = -1;
-    auto fetch = [&](Step<FMT, DH> &s, int i) {
-        if ((i & 31) == 0) {
-            page_l = pos_l = -1;
-            if (i + lane < mine) {
-                const int step = begin + warp + (i + lane) * kAttnWarps;
-                const int entry = step >> sub_shift;
-                const int id = route ? route[entry] : entry;
-                if (id >= 0 && id < p.n.table_width) {
-                    const int at = (id << p.shift) + ((step & ((1 << sub_shift) - 1)) << 4);
-                    if (at < len) {
-                        page_l = table[id];
-                        if (page_l >= 0 && page_l < p.c.pages) pos_l = at;
+    const unsigned char *stage = s_ring + warp * W::kRing, *last_pair = stage + W::kRing - 2 * W::kStage;
+    const int all_see = len - p.n.q_tokens;            // positions up to here are visible to every row
+    for (int i = 0; i < mine; ++i, stage = stage == last_pair ? stage - (W::kRing - 2 * W::kStage) : stage + 2 * W::kStage) {
+        __syncwarp();     // every lane is done with the pair that is filled now
+        fetch(i + W::kPairs - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(W::kPairs - 1) : "memory");
+        __syncwarp();
+        const int pos[2] = {queue[0][0], queue[0][1]};
+#pragma unroll
+        for (int j = 0; j + 1 < W::kPairs; ++j) queue[j][0] = queue[j + 1][0], queue[j][1] = queue[j + 1][1];
+        if (pos[0] < 0 && pos[1] < 0) continue;
+
+        // S^T: tokens g, g + 8 of each step by rows 2t, 2t + 1
+        float s[2][NT][4];
+        uint32_t vs[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const unsigned char *st = stage + u * W::kStage;
+            uint32_t ks[2], k0[W::kK], k1[W::kK];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ks[h] = read_scales<FMT, DH>(st, 0, g + 8 * h);
+                vs[u][h] = read_scales<FMT, DH>(st, 1, g + 8 * h);
+            }
+            read_key<FMT, DH>(k0, st, g, t);
+            read_key<FMT, DH>(k1, st, g + 8, t);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+            if constexpr (FMT == RR_E4M3) {
+#pragma unroll
+                for (int j = 0; j < DH / 16; ++j) {
+                    const uint32_t a[4] = {f16x2_of_e4m3(k0[j]), f16x2_of_e4m3(k1[j]), f16x2_of_e4m3(k0[j] >> 16),
+                                           f16x2_of_e4m3(k1[j] >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t b0, b1;
+                        if constexpr (NT <= 2) b0 = qf[nt][j][0], b1 = qf[nt][j][1];
+                        else query(nt, j, b0, b1);
+                        mma_f16(s[u][nt], a, b0, b1);
                     }
                 }
-            }
-        }
-        load_step(s, p, head, __shfl_sync(kFull, page_l, i & 31), __shfl_sync(kFull, pos_l, i & 31), len);
-    };
-
-    Step<FMT, DH> cur, nxt;
-    if (mine > 0) fetch(nxt, 0);
-    for (int i = 0; i < mine; ++i) {
-        cur = nxt;
-        if (i + 1 < mine) fetch(nxt, i + 1);
-        if (cur.pos < 0) continue;
-
-        // S^T: tokens g, g + 8 by rows 2t, 2t + 1
-        float s[NT][4];
+                const float kf[2] = {power_of_two(ks[0]), power_of_two(ks[1])};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        float kf[2], ev[2];
-        uint32_t gf[2] = {0, 0};
-        if constexpr (FMT == RR_E4M3) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                kf[h] = power_of_two(cur.ks[h]);
-                ev[h] = cur.vs[h] == 255 ? NAN : (float)((int)cur.vs[h] - 127);
-            }
-        } else {
-            const int grp = DH == 128 ? t : t / 2;    // the scale group of this lane's dims
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int kt = top_scale<W::kGroups>(cur.ks[h]);
-                kf[h] = has_nan<W::kGroups>(cur.ks[h]) ? NAN : power_of_two(kt);
-                const uint32_t f = group_factor((cur.ks[h] >> (8 * grp)) & 255, kt);
-                gf[h] = f | f << 16;
-                ev[h] = (float)(top_scale<W::kGroups>(cur.vs[h]) - 127 - kGroupLift);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < DH / 16; ++j) {
-            uint32_t a[4];
-            if constexpr (FMT == RR_E4M3) {
-                a[0] = f16x2_of_e4m3(cur.k[0][j] & 0xffffu);
-                a[1] = f16x2_of_e4m3(cur.k[1][j] & 0xffffu);
-                a[2] = f16x2_of_e4m3(cur.k[0][j] >> 16);
-                a[3] = f16x2_of_e4m3(cur.k[1][j] >> 16);
+                    for (int c = 0; c < 4; ++c) s[u][nt][c] = s[u][nt][c] * rowf[nt][c & 1] * kf[c >> 1];
             } else {
-                const uint32_t w0 = cur.k[0][j / 2] >> (16 * (j & 1)), w1 = cur.k[1][j / 2] >> (16 * (j & 1));
-                a[0] = mul_f16x2(f16x2_of_e2m1(w0 & 255u), gf[0]);
-                a[1] = mul_f16x2(f16x2_of_e2m1(w1 & 255u), gf[1]);
-                a[2] = mul_f16x2(f16x2_of_e2m1((w0 >> 8) & 255u), gf[0]);
-                a[3] = mul_f16x2(f16x2_of_e2m1((w1 >> 8) & 255u), gf[1]);
-            }
+                // each group's part of the score by the group's scale
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint32_t b0, b1;
-                if constexpr (NT <= 2) b0 = qf[nt][j][0], b1 = qf[nt][j][1];
-                else query(nt, j, b0, b1);
-                mma_f16(s[nt], a, b0, b1);
+                for (int grp = 0; grp < W::kGroups; ++grp) {
+                    float part[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t w0 = k0[grp] >> (16 * j), w1 = k1[grp] >> (16 * j);
+                        const uint32_t a[4] = {f16x2_of_e2m1(w0), f16x2_of_e2m1(w1), f16x2_of_e2m1(w0 >> 8),
+                                               f16x2_of_e2m1(w1 >> 8)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint32_t b0, b1;
+                            if constexpr (NT <= 2) b0 = qf[nt][2 * grp + j][0], b1 = qf[nt][2 * grp + j][1];
+                            else query(nt, 2 * grp + j, b0, b1);
+                            mma_f16(part[nt], a, b0, b1);
+                        }
+                    }
+                    const float kf[2] = {power_of_two((ks[0] >> (8 * grp)) & 255), power_of_two((ks[1] >> (8 * grp)) & 255)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[u][nt][c] = fmaf(part[nt][c], kf[c >> 1], s[u][nt][c]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[u][nt][c] *= rowf[nt][c & 1];
+            }
+        }
+
+        // The values' scales: the exponent ev that goes to a token's weight, and with
+        // groups the f16 factors of this lane's dims.  NaN scales and groups 2^26 below
+        // their row's largest are rare, and looked at once per step.
+        float ev[2][2];
+        uint32_t vf[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (FMT == RR_E4M3) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) ev[u][h] = vs[u][h] == 255 ? NAN : (float)((int)vs[u][h] - 127);
+            } else {
+                const int grp8 = (DH == 128 ? g / 2 : g / 4) * 8;
+                unsigned top[2] = {top_scale<W::kGroups>(vs[u][0]), top_scale<W::kGroups>(vs[u][1])};
+                const uint32_t both = top[0] | top[1] << 16;
+                const int from = 8 * t;                // the lane of token 2t; of 2t + 1: from + 4
+                const uint32_t w0 = __shfl_sync(kFull, vs[u][0], from), w1 = __shfl_sync(kFull, vs[u][0], from + 4);
+                const uint32_t w2 = __shfl_sync(kFull, vs[u][1], from), w3 = __shfl_sync(kFull, vs[u][1], from + 4);
+                const uint32_t ta = __shfl_sync(kFull, both, from), tb = __shfl_sync(kFull, both, from + 4);
+                const int f0 = (int)((w0 >> grp8) & 255) - (int)(ta & 0xffffu) + kGroupLift + 15;
+                const int f1 = (int)((w1 >> grp8) & 255) - (int)(tb & 0xffffu) + kGroupLift + 15;
+                const int f2 = (int)((w2 >> grp8) & 255) - (int)(ta >> 16) + kGroupLift + 15;
+                const int f3 = (int)((w3 >> grp8) & 255) - (int)(tb >> 16) + kGroupLift + 15;
+                vf[u][0] = (uint32_t)f0 << 10 | (uint32_t)f1 << 26;
+                vf[u][1] = (uint32_t)f2 << 10 | (uint32_t)f3 << 26;
+                if (__any_sync(kFull, min(min(f0, f1), min(f2, f3)) < 1 || max(top[0], top[1]) == 255)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int grp = 0; grp < W::kGroups; ++grp)
+                            if (pos[u] >= 0 && ((vs[u][h] >> (8 * grp)) & 255) == 255)
+#pragma unroll
+                                for (int r = 0; r < 2 * NT; ++r)
+                                    if (pos[u] + g + 8 * h <= pos_r[r >> 1][r & 1]) broken |= 1u << (r * W::kGroups + grp);
+                        top[h] = top_number<W::kGroups>(vs[u][h]);
+                    }
+                    vf[u][0] = group_factor((w0 >> grp8) & 255, top_number<W::kGroups>(w0)) |
+                               group_factor((w1 >> grp8) & 255, top_number<W::kGroups>(w1)) << 16;
+                    vf[u][1] = group_factor((w2 >> grp8) & 255, top_number<W::kGroups>(w2)) |
+                               group_factor((w3 >> grp8) & 255, top_number<W::kGroups>(w3)) << 16;
+                }
+                ev[u][0] = (float)((int)top[0] - 127 - kGroupLift);
+                ev[u][1] = (float)((int)top[1] - 127 - kGroupLift);
             }
         }
 
         // scores in base 2 and their masks; c: token g + 8 (c >> 1), row c & 1
+        if (cap) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[u][nt][c] = p.s2 * tanh_f32(s[u][nt][c]);
+        }
+        if (bias) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        s[u][nt][c] -= slope[nt][c & 1] *
+                                       (float)(pos_r[nt][c & 1] - near_r[nt][c & 1] - pos[u] - g - 8 * (c >> 1));
+        }
+        if (max(pos[0], pos[1]) + 15 > all_see || min(pos[0], pos[1]) < 0) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (pos[u] < 0 || pos[u] + g + 8 * (c >> 1) > pos_r[nt][c & 1]) s[u][nt][c] = -INFINITY;
+        }
+        // A masked score is -inf: its weights are zero and it moves no reference
+        // whatever its value's scale, a NaN too.
+        const float top_ev = fmaxf(fmaxf(ev[0][0], ev[0][1]), fmaxf(ev[1][0], ev[1][1]));
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int key = cur.pos + g + 8 * (c >> 1), r = c & 1;
-                float x = s[nt][c] * rowf[nt][r] * kf[c >> 1];
-                if (cap) x = p.s2 * tanhf(x);
-                if (bias) x -= slope[nt][r] * (float)(pos_r[nt][r] - key - near_r[nt][r]);
-                const bool see = key <= pos_r[nt][r];
-                if (!see) x = -INFINITY;
-                s[nt][c] = x;
-                grow = grow || x > m1[nt][r] + kSlack || (see && x - m1[nt][r] + ev[c >> 1] > m2[nt][r] + kSlack);
-                if constexpr (FMT == RR_E2M1) {
-                    if (see && has_nan<W::kGroups>(cur.vs[c >> 1])) {
-#pragma unroll
-                        for (int grp = 0; grp < W::kGroups; ++grp)
-                            if (((cur.vs[c >> 1] >> (8 * grp)) & 255) == 255)
-                                broken |= 1u << ((nt * 2 + r) * W::kGroups + grp);
-                    }
-                }
+            for (int r = 0; r < 2; ++r) {
+                // (an upper bound of the tokens' sums: at worst a move that was not needed)
+                const float a = fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r]));
+                grow = grow || a - m1[nt][r] > fminf(kSlack, m2[nt][r] + kSlack - top_ev);
             }
         if (__any_sync(kFull, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float a = fmaxf(m1[nt][r], fmaxf(s[nt][r], s[nt][2 + r]));
+                    float a = fmaxf(m1[nt][r], fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r])));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, d));
                     const float base = a == -INFINITY ? 0.f : a, down = m1[nt][r] - base;
-                    float c = fmaxf(s[nt][r] - base + ev[0], s[nt][2 + r] - base + ev[1]);
+                    float c = fmaxf(fmaxf(s[0][nt][r] - base + ev[0][0], s[0][nt][2 + r] - base + ev[0][1]),
+                                    fmaxf(s[1][nt][r] - base + ev[1][0], s[1][nt][2 + r] - base + ev[1][1]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) c = fmaxf(c, __shfl_xor_sync(kFull, c, d));
                     const float was = m2[nt][r] + down;
                     c = fmaxf(c, was);
-                    l[nt][r] *= exp2f(down);
-                    const float corr = c == -INFINITY ? 1.f : exp2f(was - c);
+                    l[nt][r] *= ex2(down);
+                    const float corr = c == -INFINITY ? 1.f : ex2(was - c);
                     m1[nt][r] = a;
                     m2[nt][r] = c;
 #pragma unroll
@@ -415,64 +585,60 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_atten
                 }
         }
 
-        // weights: P^T fragments by transposing 8x8 blocks
-        uint32_t pb[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
+        for (int u = 0; u < 2; ++u) {
+            const unsigned char *st = stage + u * W::kStage;
+            // weights: P^T fragments by transposing 8x8 blocks
+            uint32_t pb[NT][2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int r = c & 1;
-                const float x = s[nt][c];
-                const bool none = x == -INFINITY;
-                l[nt][r] += none ? 0.f : exp2f(x - m1[nt][r]);
-                w[c] = none ? 0.f : exp2f(x - m1[nt][r] + (ev[c >> 1] - m2[nt][r] + kLift));
-            }
-            pb[nt][0] = transpose_8x8(pack_f16(w[0], w[1]));
-            pb[nt][1] = transpose_8x8(pack_f16(w[2], w[3]));
-        }
-
-        // O^T: dims (DH / 8) g + 2 i (rows g) and + 1 (rows g + 8) of tile i
-        uint32_t vf[2] = {0, 0};
-        if constexpr (FMT == RR_E2M1) {
-            const int grp = DH == 128 ? g / 2 : g / 4;
-            uint32_t f[4];
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t w = __shfl_sync(kFull, cur.vs[q >> 1], 4 * (2 * t + (q & 1)));
-                f[q] = group_factor((w >> (8 * grp)) & 255, top_scale<W::kGroups>(w));
-            }
-            vf[0] = f[0] | f[1] << 16;
-            vf[1] = f[2] | f[3] << 16;
-        }
-#pragma unroll
-        for (int j = 0; j < W::kV; ++j) {
-            if constexpr (FMT == RR_E4M3) {
-                const uint32_t x0 = __byte_perm(cur.v[0][j], cur.v[1][j], 0x5140), x1 = __byte_perm(cur.v[2][j], cur.v[3][j], 0x5140);
-                const uint32_t y0 = __byte_perm(cur.v[0][j], cur.v[1][j], 0x7362), y1 = __byte_perm(cur.v[2][j], cur.v[3][j], 0x7362);
-                const uint32_t a[4] = {f16x2_of_e4m3(x0 & 0xffffu), f16x2_of_e4m3(x0 >> 16),
-                                       f16x2_of_e4m3(x1 & 0xffffu), f16x2_of_e4m3(x1 >> 16)};
-                const uint32_t c[4] = {f16x2_of_e4m3(y0 & 0xffffu), f16x2_of_e4m3(y0 >> 16),
-                                       f16x2_of_e4m3(y1 & 0xffffu), f16x2_of_e4m3(y1 >> 16)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(o[2 * j][nt], a, pb[nt][0], pb[nt][1]);
-                    mma_f16(o[2 * j + 1][nt], c, pb[nt][0], pb[nt][1]);
+                for (int c = 0; c < 4; ++c) {
+                    const int r = c & 1;
+                    // -inf - -inf: a row that has seen nothing yet
+                    const bool none = s[u][nt][c] == -INFINITY;
+                    const float x = s[u][nt][c] - m1[nt][r];
+                    l[nt][r] += none ? 0.f : ex2(x);
+                    w[c] = none ? 0.f : ex2(x + (ev[u][c >> 1] - m2[nt][r] + kLift));
                 }
-            } else {
-                // byte i of a row holds dims 2i (low half) and 2i + 1
-                const uint32_t lo0 = (cur.v[0][j] & 0x0f0f0f0fu) | (cur.v[1][j] & 0x0f0f0f0fu) << 4;
-                const uint32_t hi0 = ((cur.v[0][j] >> 4) & 0x0f0f0f0fu) | (cur.v[1][j] & 0xf0f0f0f0u);
-                const uint32_t lo1 = (cur.v[2][j] & 0x0f0f0f0fu) | (cur.v[3][j] & 0x0f0f0f0fu) << 4;
-                const uint32_t hi1 = ((cur.v[2][j] >> 4) & 0x0f0f0f0fu) | (cur.v[3][j] & 0xf0f0f0f0u);
+                pb[nt][0] = transpose_8x8(pack_f16(w[0], w[1]));
+                pb[nt][1] = transpose_8x8(pack_f16(w[2], w[3]));
+            }
+
+            // O^T: dims (DH / 8) g + 2 i (rows g) and + 1 (rows g + 8) of tile i
+            uint32_t v[4][W::kV];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t a[4] = {mul_f16x2(f16x2_of_e2m1((lo0 >> (8 * q)) & 255u), vf[0]),
-                                           mul_f16x2(f16x2_of_e2m1((hi0 >> (8 * q)) & 255u), vf[0]),
-                                           mul_f16x2(f16x2_of_e2m1((lo1 >> (8 * q)) & 255u), vf[1]),
-                                           mul_f16x2(f16x2_of_e2m1((hi1 >> (8 * q)) & 255u), vf[1])};
+            for (int q = 0; q < 4; ++q) read_value<FMT, DH>(v[q], st, 2 * t + (q & 1) + 8 * (q >> 1), g);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * j + q][nt], a, pb[nt][0], pb[nt][1]);
+            for (int j = 0; j < W::kV; ++j) {
+                if constexpr (FMT == RR_E4M3) {
+                    const uint32_t x0 = __byte_perm(v[0][j], v[1][j], 0x5140), x1 = __byte_perm(v[2][j], v[3][j], 0x5140);
+                    const uint32_t y0 = __byte_perm(v[0][j], v[1][j], 0x7362), y1 = __byte_perm(v[2][j], v[3][j], 0x7362);
+                    const uint32_t a[4] = {f16x2_of_e4m3(x0), f16x2_of_e4m3(x0 >> 16), f16x2_of_e4m3(x1),
+                                           f16x2_of_e4m3(x1 >> 16)};
+                    const uint32_t c[4] = {f16x2_of_e4m3(y0), f16x2_of_e4m3(y0 >> 16), f16x2_of_e4m3(y1),
+                                           f16x2_of_e4m3(y1 >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(o[2 * j][nt], a, pb[nt][0], pb[nt][1]);
+                        mma_f16(o[2 * j + 1][nt], c, pb[nt][0], pb[nt][1]);
+                    }
+                } else {
+                    // byte i of a row holds dims 2i (low half) and 2i + 1
+                    const uint32_t lo0 = (v[0][j] & 0x0f0f0f0fu) | (v[1][j] & 0x0f0f0f0fu) << 4;
+                    const uint32_t hi0 = ((v[0][j] >> 4) & 0x0f0f0f0fu) | (v[1][j] & 0xf0f0f0f0u);
+                    const uint32_t lo1 = (v[2][j] & 0x0f0f0f0fu) | (v[3][j] & 0x0f0f0f0fu) << 4;
+                    const uint32_t hi1 = ((v[2][j] >> 4) & 0x0f0f0f0fu) | (v[3][j] & 0xf0f0f0f0u);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t a[4] = {mul_f16x2(f16x2_of_e2m1(lo0 >> (8 * q)), vf[u][0]),
+                                               mul_f16x2(f16x2_of_e2m1(hi0 >> (8 * q)), vf[u][0]),
+                                               mul_f16x2(f16x2_of_e2m1(lo1 >> (8 * q)), vf[u][1]),
+                                               mul_f16x2(f16x2_of_e2m1(hi1 >> (8 * q)), vf[u][1])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * j + q][nt], a, pb[nt][0], pb[nt][1]);
+                    }
                 }
             }
         }
@@ -500,94 +666,98 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT <= 2 ? 2 : 1) cached_atten
         }
     }
 
-    // the warps' results, joined in pairs: the upper half hands its state to the lower
-    for (int half = kAttnWarps / 2; half; half >>= 1) {
-        float *at = s_merge + (warp - half) * 32 * kKeep + lane;
-        if (warp >= half && warp < 2 * half) {
-            int k = 0;
+    // The warps' results, joined through the ring's memory: every warp leaves
+    // its state, and takes (tile of dims, tile of rows) pairs to join.
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+#if __CUDA_ARCH__ >= 900
+    cudaTriggerProgrammaticLaunchCompletion();
+#endif
+    {
+        float *at = s_merge + warp * 32 * kKeep + lane;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int i = 0; i < kMT; ++i)
+            for (int i = 0; i < kMT; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) at[32 * k++] = o[i][nt][c];
+                for (int c = 0; c < 4; ++c) at[32 * ((nt * kMT + i) * 4 + c)] = o[i][nt][c];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    at[32 * k++] = m1[nt][r];
-                    at[32 * k++] = m2[nt][r];
-                    at[32 * k++] = l[nt][r];
-                }
+            for (int r = 0; r < 2; ++r) {
+                float *st = at + 32 * (NT * kMT * 4 + nt * 6 + 3 * r);
+                st[0] = m1[nt][r];
+                st[32] = m2[nt][r];
+                st[64] = l[nt][r];
             }
         }
-        __syncthreads();
-        if (warp < half) {
-            at = s_merge + warp * 32 * kKeep + lane;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float *os = at + 32 * (nt * (kMT * 4 + 6)), *st = os + 32 * kMT * 4;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float a = st[32 * 3 * r], c = st[32 * (3 * r + 1)], ls = st[32 * (3 * r + 2)];
-                    const float n1 = fmaxf(m1[nt][r], a), b1 = n1 == -INFINITY ? 0.f : n1;
-                    l[nt][r] = l[nt][r] * exp2f(m1[nt][r] - b1) + ls * exp2f(a - b1);
-                    const float r0 = m2[nt][r] + (m1[nt][r] - b1), r1 = c + (a - b1), n2 = fmaxf(r0, r1);
-                    const float b2 = n2 == -INFINITY ? 0.f : n2;
-                    const float f0 = exp2f(r0 - b2), f1 = exp2f(r1 - b2);
-                    m1[nt][r] = n1;
-                    m2[nt][r] = n2;
-#pragma unroll
-                    for (int i = 0; i < kMT; ++i) {
-                        o[i][nt][r] = o[i][nt][r] * f0 + os[32 * (4 * i + r)] * f1;
-                        o[i][nt][2 + r] = o[i][nt][2 + r] * f0 + os[32 * (4 * i + 2 + r)] * f1;
-                    }
-                }
-            }
-        }
-        __syncthreads();
     }
-    if (warp != 0) return;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    __syncthreads();
+    for (int pair = warp; pair < kMT * NT; pair += kAttnWarps) {
+        const int nt = pair / kMT, i = pair % kMT;
+        const float *at = s_merge + lane;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = row0 + nt * 8 + 2 * t + r;
             if (row >= p.rows) continue;
-            const int dim = (DH / 8) * g;
+            const float *st = at + 32 * (NT * kMT * 4 + nt * 6 + 3 * r), *os = at + 32 * (pair * 4 + r);
+            float a[kAttnWarps], c[kAttnWarps], n1 = -INFINITY, n2 = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                a[w] = st[w * 32 * kKeep];
+                n1 = fmaxf(n1, a[w]);
+            }
+            const float b1 = n1 == -INFINITY ? 0.f : n1;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                a[w] -= b1;
+                c[w] = st[w * 32 * kKeep + 32] + a[w];
+                n2 = fmaxf(n2, c[w]);
+            }
+            const float b2 = n2 == -INFINITY ? 0.f : n2;
+            float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = ex2(c[w] - b2);
+                sum += st[w * 32 * kKeep + 64] * ex2(a[w]);
+                x += os[w * 32 * kKeep] * f;
+                y += os[w * 32 * kKeep + 64] * f;
+            }
+            const int dim = (DH / 8) * g + 2 * i;
+            const int back = p.n.q_tokens - 1 - row / p.group, near = max(0, *s_near - back);
             if (p.splits > 1) {
-                float *at = p.part + (((size_t)blockIdx.y * p.splits + blockIdx.x) * p.rows + row) * (DH + kState);
-#pragma unroll
-                for (int i = 0; i < kMT; ++i)
-                    *reinterpret_cast<float2 *>(at + dim + 2 * i) = make_float2(o[i][nt][r], o[i][nt][2 + r]);
-                if (g == 0) *reinterpret_cast<float4 *>(at + DH) = make_float4(m1[nt][r], l[nt][r], m2[nt][r], (float)near_r[nt][r]);
+                float *part = p.part + (((size_t)blockIdx.y * p.splits + blockIdx.x) * p.rows + row) * (DH + kState);
+                *reinterpret_cast<float2 *>(part + dim) = make_float2(x, y);
+                if (g == 0 && i == 0) *reinterpret_cast<float4 *>(part + DH) = make_float4(n1, sum, n2, (float)near);
             } else {
-                const bool none = l[nt][r] == 0.f;
-                const float f = none ? 0.f : exp2f(m2[nt][r] - kLift) / l[nt][r];
+                const bool none = sum == 0.f;
+                const float f = none ? 0.f : ex2(n2 - kLift) / sum;
+                x = none ? 0.f : x * f;
+                y = none ? 0.f : y * f;
                 const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
-                uint32_t *out = static_cast<uint32_t *>(p.a.out) + (orow * DH + dim) / 2;
-#pragma unroll
-                for (int i = 0; i < kMT; ++i) {
-                    const float x = none ? 0.f : o[i][nt][r] * f, y = none ? 0.f : o[i][nt][2 + r] * f;
-                    out[i] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
-                }
-                if (p.a.lse && g == 0)
+                static_cast<uint32_t *>(p.a.out)[(orow * DH + dim) / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
+                if (p.a.lse && g == 0 && i == 0)
                     p.a.lse[orow] = none ? -INFINITY
-                                         : (m1[nt][r] + log2f(l[nt][r])) * kLn2 - (bias ? slope[nt][r] * kLn2 * (float)near_r[nt][r] : 0.f);
+                                         : (n1 + log2f(sum)) * kLn2 -
+                                               (bias ? p.a.slopes[head * p.group + row % p.group] * (float)near : 0.f);
             }
         }
+    }
 }
 
-// Joins the splits of one row: a warp per row, a lane DH / 32 dims.
+// Joins the splits of one row: a block per row, its warps take splits in turn,
+// a lane DH / 32 dims.  Launched while the attention's last blocks still run
+// (its results are waited for below), which hides the launch.
 template <int DH>
-__global__ void __launch_bounds__(128) cached_join_kernel(const __grid_constant__ Cached p, long long rows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __grid_constant__ Cached p) {
     constexpr int E = DH / 32;
-    const int lane = threadIdx.x & 31;
-    const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    const long long bh = r / p.rows;
-    const int row = (int)(r % p.rows), head = (int)(bh % p.c.heads);
-    const long long b = bh / p.c.heads;
+    __shared__ float s_o[kJoinWarps][DH], s_l[kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bh = blockIdx.x / p.rows, row = blockIdx.x % p.rows, head = bh % p.c.heads, b = bh / p.c.heads;
+    const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
     const float *at = p.part + ((size_t)bh * p.splits * p.rows + row) * (DH + kState);
     const size_t stride = (size_t)p.rows * (DH + kState);
+#if __CUDA_ARCH__ >= 900
+    cudaGridDependencySynchronize();
+#endif
     float n1 = -INFINITY, n2 = -INFINITY;
     for (int s = lane; s < p.splits; s += 32) n1 = fmaxf(n1, at[s * stride + DH]);
 #pragma unroll
@@ -601,27 +771,40 @@ __global__ void __launch_bounds__(128) cached_join_kernel(const __grid_constant_
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-        const float4 st = *reinterpret_cast<const float4 *>(at + s * stride + DH);
-        l += st.y * exp2f(st.x - b1);
-        const float f = exp2f(st.z + (st.x - b1) - b2);
+    for (int s = warp; s < p.splits; s += kJoinWarps) {
+        const float *x = at + s * stride;
+        const float4 st = *reinterpret_cast<const float4 *>(x + DH);
+        float v[E];
+        if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x + lane * 4);
+        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(x + lane * 2);
+        l += st.y * ex2(st.x - b1);
+        const float f = ex2(st.z + (st.x - b1) - b2);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += at[s * stride + lane * E + e] * f;
+        for (int e = 0; e < E; ++e) o[e] += v[e] * f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (threadIdx.x >= DH / 2) return;
+    const int d = 2 * threadIdx.x;
+    float x = 0.f, y = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        l += s_l[w];
+        x += s_o[w][d];
+        y += s_o[w][d + 1];
     }
     const bool none = l == 0.f;
-    const float f = none ? 0.f : exp2f(n2 - kLift) / l;
-    const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
-    uint32_t *out = static_cast<uint32_t *>(p.a.out) + (orow * DH + lane * E) / 2;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        const float x = none ? 0.f : o[e] * f, y = none ? 0.f : o[e + 1] * f;
-        out[e / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
-    }
-    if (p.a.lse && lane == 0) {
-        const float near = at[DH + 3];
+    const float f = none ? 0.f : ex2(n2 - kLift) / l;
+    x = none ? 0.f : x * f;
+    y = none ? 0.f : y * f;
+    static_cast<uint32_t *>(p.a.out)[(orow * DH + d) / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
+    if (p.a.lse && threadIdx.x == 0)
         p.a.lse[orow] = none ? -INFINITY
-                             : (n1 + log2f(l)) * kLn2 - (p.a.slopes ? p.a.slopes[head * p.group + row % p.group] * near : 0.f);
-    }
+                             : (n1 + log2f(l)) * kLn2 -
+                                   (p.a.slopes ? p.a.slopes[head * p.group + row % p.group] * at[DH + 3] : 0.f);
 }
 
 bool config_ok(const rr_cache_config *c, const rr_cached_attn_config *n) {
@@ -645,23 +828,36 @@ int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
-// CTAs that share a sequence's tokens: enough of them for four waves of two
-// CTAs on each of 148 SMs, so that ragged lengths even out, but at least one
-// step of 16 tokens for each of a CTA's warps.
+// CTAs that share a sequence's tokens.  A CTA costs its share of the steps and
+// a start and an end worth about 24 of them; CTAs come in waves of 148 SMs, of
+// which the last is half empty when there is more than one.  Measured: 16
+// sequences of 512 steps and 8 heads, 2 CTAs each (256 in one wave) 72 us, 3
+// (two waves) 88 us; 64 sequences of up to 751 steps, 1 CTA each 250 us, 2
+// 216 us, 3 223 us.  No CTA gets less than a pair of steps for each warp.
 int splits_of(const rr_cache_config *c, const rr_cached_attn_config *n, bool route) {
     const long long rows = (long long)(n->q_heads / c->heads) * n->q_tokens;
-    const long long blocks = (long long)n->batch * c->heads * ((rows + 8 * tiles_of(c, n) - 1) / (8 * tiles_of(c, n)));
+    const int nt = tiles_of(c, n), slots = 148 * ctas_per_sm(c->dh, nt);
+    const long long blocks = (long long)n->batch * c->heads * ((rows + 8 * nt - 1) / (8 * nt));
     const long long steps = (long long)(route ? n->width : n->table_width) * (c->chunk / 16);
     if (blocks == 0) return 1;
-    const long long want = (4 * 296 + blocks - 1) / blocks, most = steps / kAttnWarps;
-    const long long s = want < most ? want : most;
-    return s < 1 ? 1 : (int)s;
+    const long long most = steps / (2 * kAttnWarps), tried = 4 * slots / blocks + 1;
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s == 1 || (s <= most && s <= tried); ++s) {
+        const double ctas = (double)blocks * s, waves = ctas <= slots ? 1.0 : ctas / slots + 0.5;
+        const double cost = waves * ((double)steps / s + 24.0);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
 }
 
 template <int FMT, int DH, int NT>
 cudaError_t launch(const Cached &p, cudaStream_t s) {
     constexpr int kKeep = DH / 16 * 4 * NT + 6 * NT;
-    const int smem = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 + kAttnWarps / 2 * 32 * kKeep * 4;
+    using W = Words<FMT, DH>;
+    const int ring = kAttnWarps * W::kRing, merge = kAttnWarps * 32 * kKeep * 4;
+    const int smem = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 +
+                     (ring > merge ? ring : merge);
     auto kern = cached_attention_kernel<FMT, DH, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -669,9 +865,16 @@ cudaError_t launch(const Cached &p, cudaStream_t s) {
     kern<<<grid, 32 * kAttnWarps, smem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    const long long rows = (long long)p.n.batch * p.c.heads * p.rows;
-    cached_join_kernel<DH><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p, rows);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = dim3((unsigned)p.n.batch * p.c.heads * p.rows);
+    join.blockDim = dim3(32 * kJoinWarps);
+    join.stream = s;
+    join.attrs = &early;
+    join.numAttrs = 1;
+    return cudaLaunchKernelEx(&join, cached_join_kernel<DH>, p);
 }
 
 template <int FMT, int DH>

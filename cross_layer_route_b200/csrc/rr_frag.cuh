@@ -76,6 +76,30 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// 2^x by the special function unit (relative error 2^-22; results below 2^-126 are zero).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh z.  Below 0.35 its Taylor series, whose first term left out is 1.2e-8 of
+// z there; above it 1 - 2 / (1 + e^2z), where the difference loses at most two
+// bits: relative error 2^-21 over the whole range, so a cap far above the
+// scores leaves them as they are.
+__device__ __forceinline__ float tanh_series(float z) {
+    const float y = z * z;
+    float s = fmaf(y, -0.00886323553f, 0.0218694885f);
+    s = fmaf(y, s, -0.0539682540f);
+    s = fmaf(y, s, 0.133333333f);
+    s = fmaf(y, s, -0.333333333f);
+    return fmaf(z * y, s, z);
+}
+__device__ __forceinline__ float tanh_f32(float z) {
+    const float far = 1.f - __fdividef(2.f, 1.f + ex2(z * 2.8853900817779268f));
+    return fabsf(z) < 0.35f ? tanh_series(z) : far;
+}
+
 // The two 16-bit types of the operators that take either.
 template <typename T>
 struct Half;

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
 #pragma unroll
             for (int n = 0; n < kSlots / 8; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[n][c] = p.s2 * tanhf(s[n][c] * p.s1);
+                for (int c = 0; c < 4; ++c) s[n][c] = p.s2 * tanh_f32(s[n][c] * p.s1);
         } else {
 #pragma unroll
             for (int n = 0; n < kSlots / 8; ++n)
