@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librr.so")
 SOURCES = ["rr_api.cu", "rr_route_simt.cu", "rr_route_tc.cu", "rr_select_tc.cu", "rr_relay.cu", "rr_noalloc.cu",
            "rr_attention.cu", "rr_masked.cu",
-           "rr_cache.cu", "rr_cached.cu"]
+           "rr_masked_tc.cu", "rr_cache.cu", "rr_cached.cu"]
 HEADERS = ["rr_device.cuh", "rr_internal.h", "rr_tc.cuh", "rr_frag.cuh", "rr_masked.cuh", "rr_cache.cuh"]
 
 

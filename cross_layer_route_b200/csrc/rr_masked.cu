@@ -352,7 +352,9 @@ extern "C" rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const
     const unsigned units = (unsigned)((long long)cfg->batch * cfg->route_heads * p.nqc);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (cfg->dtype == RR_BF16)
+    if (tc_takes(p))
+        e = launch_tc(p, units, s);
+    else if (cfg->dtype == RR_BF16)
         e = cfg->dh == 64 ? launch<__nv_bfloat16, 64>(p, units, s) : launch<__nv_bfloat16, 128>(p, units, s);
     else
         e = cfg->dh == 64 ? launch<__half, 64>(p, units, s) : launch<__half, 128>(p, units, s);

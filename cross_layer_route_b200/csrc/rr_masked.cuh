@@ -208,4 +208,8 @@ __device__ __noinline__ void row_alone(const Masked &p, const Unit &u, const int
     for (int e = 0; e < E; ++e) out[e] = Half<T>::down(l == 0.f ? 0.f : o[e] / l);
 }
 
+// The kernel on tcgen05 (rr_masked_tc.cu): whether it takes the problem, and its launch.
+bool tc_takes(const Masked &p);
+cudaError_t launch_tc(const Masked &p, unsigned units, cudaStream_t s);
+
 }  // namespace rr_masked
