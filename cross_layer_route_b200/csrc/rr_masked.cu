@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
         if (ok1) lse[8] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * kLn2 - unit * (float)near1;
     }
     // rows to compute on their own, one bit for each of the warp's 16
-    const unsigned b0 = __ballot_sync(kFull, bad0 && ok0 && l0 != 0.f);
-    const unsigned b1 = __ballot_sync(kFull, bad1 && ok1 && l1 != 0.f);
+    // (where the sum is a NaN, a score that the row sees is one, and so is the row)
+    const unsigned b0 = __ballot_sync(kFull, bad0 && ok0 && l0 != 0.f && l0 == l0);
+    const unsigned b1 = __ballot_sync(kFull, bad1 && ok1 && l1 != 0.f && l1 == l1);
     for (int r = 0; r < 16 && (b0 | b1); ++r) {
         if (!(((r < 8 ? b0 : b1) >> (4 * (r & 7))) & 15u)) continue;
         const int near = __shfl_sync(kFull, r < 8 ? near0 : near1, 4 * (r & 7));

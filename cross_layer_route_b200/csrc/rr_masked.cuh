@@ -59,17 +59,19 @@ __device__ __forceinline__ Unit unit_of(const Masked &p, unsigned block) {
     return u;
 }
 
-// Smallest and largest of n int32 at x, by a warp.
-__device__ __forceinline__ void warp_min_max(const int32_t *x, int n, int &lo, int &hi) {
+// Smallest and largest of n <= 128 int32 at x: this lane's part.
+__device__ __forceinline__ void lane_min_max(const int32_t *x, int n, int &lo, int &hi) {
     lo = INT_MAX;
     hi = INT_MIN;
-    for (int e = threadIdx.x & 31; e < n; e += 32) {
-        const int v = x[e];
-        lo = min(lo, v);
-        hi = max(hi, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = (threadIdx.x & 31) + 32 * i;
+        if (e < n) {
+            const int v = x[e];
+            lo = min(lo, v);
+            hi = max(hi, v);
+        }
     }
-    lo = __reduce_min_sync(kFull, lo);
-    hi = __reduce_max_sync(kFull, hi);
 }
 
 // The unit's route in shared memory: list[0..n-1] = key chunks that can hold a
@@ -96,21 +98,32 @@ __device__ __forceinline__ int build_list(const Masked &p, const Unit &u, int32_
         }
         list[e] = j;
     }
+    int qlo = 0, qhi = 0;
+    if (docs) lane_min_max(p.a.doc_q + (size_t)u.b * p.c.nq_tokens + (u.i << p.shift), u.tokens, qlo, qhi);
     __syncthreads();
     if (docs) {
         // documents are mostly runs of tokens: a chunk of one document is either
         // visible to a query chunk of one document as a whole or not at all
-        int qlo, qhi;
-        warp_min_max(p.a.doc_q + (size_t)u.b * p.c.nq_tokens + (u.i << p.shift), u.tokens, qlo, qhi);
-        for (int e = warp; e < width; e += warps) {
-            const int j = list[e];
-            if (j < 0) continue;
-            const int lo = (j & kChunkId) << p.shift;
-            int klo, khi;
-            warp_min_max(p.a.doc_k + (size_t)u.b * p.c.nk_tokens + lo, min(p.c.chunk, p.c.nk_tokens - lo), klo, khi);
-            if (lane == 0) {
-                if (khi < 0 || qhi < 0 || khi < qlo || klo > qhi) list[e] = -1;
-                else if (klo != khi || qlo != qhi) list[e] = j & ~kChunkFull;
+        qlo = __reduce_min_sync(kFull, qlo);
+        qhi = __reduce_max_sync(kFull, qhi);
+        constexpr int kAtOnce = 4;     // entries whose loads are in flight together
+        for (int e0 = warp * kAtOnce; e0 < width; e0 += warps * kAtOnce) {
+            int j[kAtOnce], klo[kAtOnce], khi[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                j[i] = e0 + i < width ? list[e0 + i] : -1;
+                const int lo = j[i] < 0 ? 0 : (j[i] & kChunkId) << p.shift;
+                lane_min_max(p.a.doc_k + (size_t)u.b * p.c.nk_tokens + lo,
+                             j[i] < 0 ? 0 : min(p.c.chunk, p.c.nk_tokens - lo), klo[i], khi[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                klo[i] = __reduce_min_sync(kFull, klo[i]);
+                khi[i] = __reduce_max_sync(kFull, khi[i]);
+                if (lane == 0 && j[i] >= 0) {
+                    if (khi[i] < 0 || qhi < 0 || khi[i] < qlo || klo[i] > qhi) list[e0 + i] = -1;
+                    else if (klo[i] != khi[i] || qlo != qhi) list[e0 + i] = j[i] & ~kChunkFull;
+                }
             }
         }
         __syncthreads();

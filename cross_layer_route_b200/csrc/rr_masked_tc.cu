@@ -47,7 +47,7 @@ struct TcShape {
     static constexpr int kTileBytes = kSubs * kSubBytes;          // a Q, K or V tile
     static constexpr int kStages = DH == 128 ? 4 : 8;
     static constexpr int kHead = kMaxWidth * 4 + 16;
-    static constexpr int kBars = 2 * kStages + 3 * kTiles + 2;
+    static constexpr int kBars = 2 * kStages + 4 * kTiles + 2;
     static constexpr int kMisc = 256;
     static constexpr int kSmem = 1024 + kHead + kBars * 8 + kMisc + (kTiles + kStages) * kTileBytes;
 };
@@ -77,6 +77,19 @@ __device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMa
         "l"(reinterpret_cast<uint64_t>(map)), "r"(saddr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
+// Tensor maps of the operands; axes: see tensor_map.
+struct Maps {
+    CUtensorMap q, k, v, out;
+    int axes[4];
+};
 
 // 32 columns of this thread's TMEM lane; the values may be used after wait_ld32.
 __device__ __forceinline__ void ld32(uint32_t taddr, float *v) {
@@ -120,12 +133,17 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// (NaN if any of them is)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kTcThreads, 1)
-masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_constant__ CUtensorMap map_k,
-                           const __grid_constant__ CUtensorMap map_v, int k_axes, int v_axes) {
+masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_constant__ Maps maps) {
     using S = TcShape<DH>;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = align_smem_1024(raw);
@@ -134,7 +152,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     int32_t *s_n = s_list + kMaxWidth;
     uint64_t *full = reinterpret_cast<uint64_t *>(s_list + kMaxWidth + 4);
     uint64_t *empty = full + S::kStages, *s_full = empty + S::kStages, *p_ready = s_full + kTiles;
-    uint64_t *o_done = p_ready + kTiles, *q_ready = o_done + kTiles, *mma_done = q_ready + 1;
+    uint64_t *o_done = p_ready + 2 * kTiles, *q_ready = o_done + kTiles, *mma_done = q_ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -149,10 +167,11 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
         }
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_ready[t], 4);
+            mbar_init(&p_ready[2 * t], 4);
+            mbar_init(&p_ready[2 * t + 1], 4);
             mbar_init(&o_done[t], 1);
         }
-        mbar_init(q_ready, 4 * tiles);
+        mbar_init(q_ready, 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -179,25 +198,6 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             const int head = u.route_head * p.group + (in_unit ? row >> p.shift : 0), tok = row & (p.c.chunk - 1);
             const bool valid = in_unit && tok < u.tokens;
             const int64_t token = ((int64_t)u.i << p.shift) + tok;
-            if (n > 0) {
-                // this warp's 32 rows of Q into the layout a swizzled TMA load would give
-                constexpr int kPer = DH / 8;
-                unsigned char *dst = q_s + t * S::kTileBytes;
-                for (int e = lane; e < 32 * kPer; e += 32) {
-                    const int r = (warp & 3) * 32 + e / kPer, c = e % kPer, ur = row0 + t * kTileRows + r;
-                    const int utok = ur & (p.c.chunk - 1);
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (ur < rows && utok < u.tokens)
-                        w = *reinterpret_cast<const uint4 *>(
-                            static_cast<const T *>(p.a.q) + u.b * p.c.q_stride[0] +
-                            (u.route_head * p.group + (ur >> p.shift)) * p.c.q_stride[1] +
-                            (((int64_t)u.i << p.shift) + utok) * p.c.q_stride[2] + c * 8);
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * kSubBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready);
-            }
             const int pos = u.p_first + tok;
             const bool docs = p.a.doc_q != nullptr, bias = p.a.slopes != nullptr, cap = p.c.soft_cap > 0.f;
             const int doc = docs && valid ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + token] : -1;
@@ -225,9 +225,12 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 for (int c = 0; c < kTileKeys; c += 32) wait_ld32(s + c);
                 if (cap) {
                     // z = s1 s; the polynomial alone while no score of the warp reaches the cap
-                    float most = 0.f;
+                    float tops[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < kTileKeys; ++c) most = fmaxf(most, fabsf(s[c]));
+                    for (int c = 0; c < kTileKeys; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], fabsf(s[c + 2 * i]), fabsf(s[c + 2 * i + 1]));
+                    const float most = max3(max3(tops[0], tops[1], tops[2]), tops[3], tops[3]);
                     if (__all_sync(kFull, most * p.s1 < 1.f)) {
 #pragma unroll
                         for (int c = 0; c < kTileKeys; ++c) s[c] = p.s2 * rr_attn::tanh_within_one(s[c] * p.s1);
@@ -237,32 +240,46 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     }
                 }
                 const float scale = cap ? 1.f : p.s1;
+                // what a tile's chunks are to the unit: lane e looks at chunk e of the tile
+                const int per = kTileKeys >> p.shift;
+                const int mine = j * per + lane < n_list ? s_list[j * per + lane] : -1;
+                const bool plain = __all_sync(kFull, lane >= per || (mine >= 0 && (mine & kChunkFull)));
+                if (bias) {
 #pragma unroll
-                for (int c0 = 0; c0 < kTileKeys; c0 += 16) {
-                    const int at = (j * kTileKeys + c0) >> p.shift;
-                    const int entry = at < n_list ? s_list[at] : -1;
-                    const int base = entry < 0 ? 0 : ((entry & kChunkId) << p.shift) + (c0 & (p.c.chunk - 1));
-                    if (bias) {
-                        const float from = (float)(pos - base);
+                    for (int c0 = 0; c0 < kTileKeys; c0 += 16) {
+                        const int entry = __shfl_sync(kFull, mine, c0 >> p.shift) & kChunkId;
+                        const float from = (float)(pos - ((entry << p.shift) + (c0 & (p.c.chunk - 1))));
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             s[c0 + c] = s[c0 + c] * scale - slope * (fabsf(from - (float)c) - (float)near);
                     }
-                    if (entry < 0 || !(entry & kChunkFull)) {
-                        const int left = entry < 0 ? 0 : limit - base;
+                }
+                if (!plain) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            bool see = c < left;
-                            if (docs && see) see = doc >= 0 && doc_k[base + c] == doc;
-                            if (!see) s[c0 + c] = -INFINITY;
+                    for (int c0 = 0; c0 < kTileKeys; c0 += 16) {
+                        const int entry = __shfl_sync(kFull, mine, c0 >> p.shift);
+                        if (entry >= 0 && (entry & kChunkFull)) continue;
+                        const int base = entry < 0 ? 0 : ((entry & kChunkId) << p.shift) + (c0 & (p.c.chunk - 1));
+                        const int left = entry < 0 ? 0 : limit - base;
+                        if (docs) {
+                            int dk[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) dk[c] = doc_k[min(base + c, p.c.nk_tokens - 1)];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) s[c0 + c] = c < left && dk[c] == doc && doc >= 0 ? s[c0 + c] : -INFINITY;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) s[c0 + c] = c < left ? s[c0 + c] : -INFINITY;
                         }
                     }
                 }
                 const float mul = bias ? 1.f : scale;
-                float top = -INFINITY;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < kTileKeys; ++c) top = fmaxf(top, s[c]);
-                top *= mul;
+                for (int c = 0; c < kTileKeys; c += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], s[c + 2 * i], s[c + 2 * i + 1]);
+                const float top = max3(max3(tops[0], tops[1], tops[2]), tops[3], tops[3]) * mul;
                 if (__any_sync(kFull, top > m + kSlack)) {
                     const float was = m;
                     m = fmaxf(m, top);
@@ -283,34 +300,41 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : kLift - m;
-                float sum = 0.f;
+                // an infinite or NaN score makes the row NaN
+                const float ref = !(top < INFINITY) ? NAN : m == -INFINITY ? 0.f : kLift - m;
+                float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c0 = 0; c0 < kTileKeys; c0 += 32) {
-                    uint32_t w[16];
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float x = rr_attn::ex2(fmaf(s[c0 + 2 * c], mul, ref));
-                        const float y = rr_attn::ex2(fmaf(s[c0 + 2 * c + 1], mul, ref));
-                        sum += x + y;
-                        w[c] = Half<T>::pack(x, y);
+                    for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float x = rr_attn::ex2(fmaf(s[c0 + 2 * c], mul, ref));
+                            const float y = rr_attn::ex2(fmaf(s[c0 + 2 * c + 1], mul, ref));
+                            sums[2 * (c & 1)] += x;
+                            sums[2 * (c & 1) + 1] += y;
+                            w[c] = Half<T>::pack(x, y);
+                        }
+                        st16(s_at + c0 / 2, w);
                     }
-                    st16(s_at + c0 / 2, w);
+                    wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[2 * t + half]);
                 }
-                l += sum;
-                wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[t]);
+                l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             }
             if (ok && n > 0) {
                 ok = mbar_wait_warp(&o_done[t], (n - 1) & 1, abort_flag);
                 tc_fence_after();
             }
-            // a row that saw nothing is zero whatever its accumulators hold
-            T *out = static_cast<T *>(p.a.out) + u.b * p.c.out_stride[0] + head * p.c.out_stride[1] + token * p.c.out_stride[2];
+            // Rows go out by TMA from where Q lay (every product that read it is done), a
+            // warp's 32 rows by itself.  A row that saw nothing is zero whatever its
+            // accumulators hold.
             const float inv = l == 0.f ? 0.f : 1.f / l;
             bool bad = false;
+            unsigned char *dst = q_s + t * S::kTileBytes + (threadIdx.x & 127) * 128;
 #pragma unroll
             for (int c0 = 0; c0 < DH; c0 += 32) {
                 float o[32];
@@ -326,18 +350,37 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     bad = bad || !isfinite(o[2 * c]) || !isfinite(o[2 * c + 1]);
                     w[c] = Half<T>::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
                 }
-                if (valid) {
 #pragma unroll
-                    for (int c = 0; c < 16; c += 4)
-                        *reinterpret_cast<uint4 *>(out + c0 + 2 * c) = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(dst + (c0 >> 6) * kSubBytes + ((((c0 & 63) / 8 + c) ^ (lane & 7)) << 4)) =
+                        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                const int rows_out = min(32, p.c.chunk);
+                for (int r = 0; r < 32; r += rows_out) {
+                    const int ur = row0 + warp * 32 + r;       // of the unit; 32 warp: tile and row
+                    if (ur >= rows) break;
+                    for (int sub = 0; sub < S::kSubs; ++sub)
+                        tma_store_4d(&maps.out, saddr(q_s) + t * S::kTileBytes + sub * kSubBytes + ((warp & 3) * 32 + r) * 128,
+                                     sub * 64, (u.i << p.shift) + (ur & (p.c.chunk - 1)),
+                                     u.route_head * p.group + (ur >> p.shift), u.b);
                 }
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             if (valid && p.a.lse)
                 p.a.lse[((size_t)u.b * p.c.q_heads + head) * p.c.nq_tokens + token] =
                     !ok ? NAN
                         : l == 0.f ? -INFINITY
                                    : (m - kLift + log2f(l)) * kLn2 - (bias ? p.a.slopes[head] * (float)near : 0.f);
-            unsigned again = __ballot_sync(kFull, ok && bad && valid);
+            // (where the sum is a NaN, a score that the row sees is one, and so is the row)
+            unsigned again = __ballot_sync(kFull, ok && bad && valid && l == l);
+            if (lane == 0) {
+                if (again) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();
             while (again) {
                 const int r = __ffs(again) - 1;
                 again &= again - 1;
@@ -349,14 +392,26 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
         if (warp == kSoftWarps + 1) {
             // ---- producer: K_0, V_0, K_1, V_1, ... ----
             const int box = p.c.chunk, per = kTileKeys >> p.shift;
-            const int kh = k_axes & 1 ? u.kv_head : 0, kb = k_axes & 2 ? u.b : 0;
-            const int vh = v_axes & 1 ? u.kv_head : 0, vb = v_axes & 2 ? u.b : 0;
+            const int kh = maps.axes[1] & 1 ? u.kv_head : 0, kb = maps.axes[1] & 2 ? u.b : 0;
+            const int vh = maps.axes[2] & 1 ? u.kv_head : 0, vb = maps.axes[2] & 2 ? u.b : 0;
+            if (n > 0) {
+                // the heads of the tiles' rows; rows past the unit as tokens past the last, which read as zeros
+                mbar_expect_tx_elect(q_ready, tiles * S::kTileBytes);
+                for (int e = 0; e < tiles * per; ++e) {
+                    const int h = (row0 >> p.shift) + e;
+                    const int head = maps.axes[0] & 1 ? u.route_head * p.group + min(h, p.group - 1) : 0;
+                    const int token = h < p.group ? u.i << p.shift : p.c.nq_tokens;
+                    for (int sub = 0; sub < S::kSubs; ++sub)
+                        tma_load_4d_elect(saddr(q_s) + e / per * S::kTileBytes + sub * kSubBytes + e % per * box * 128,
+                                          &maps.q, q_ready, sub * 64, token, head, maps.axes[0] & 2 ? u.b : 0);
+                }
+            }
             int issued = 0;
             for (int g = 0; g < 2 * n; ++g) {
                 const int s = g % S::kStages;
                 if (g >= S::kStages && !mbar_wait_warp(&empty[s], ((g / S::kStages) & 1) ^ 1, abort_flag)) break;
                 mbar_expect_tx_elect(&full[s], S::kTileBytes);
-                const CUtensorMap *map = g & 1 ? &map_v : &map_k;
+                const CUtensorMap *map = g & 1 ? &maps.v : &maps.k;
                 const uint32_t dst = saddr(kv_s) + s * S::kTileBytes;
                 for (int e = 0; e < per; ++e) {
                     // past the route: a box past the tokens, which reads as zeros
@@ -368,7 +423,12 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 }
                 ++issued;
             }
-            // every issued stage must have landed before the CTA exits
+            // every issued copy must have landed before the CTA exits
+            if (n > 0) {
+                const long long t0 = clock64();
+                while (!mbar_test(q_ready, 0) && clock64() - t0 < kSpinLimit) {
+                }
+            }
             for (int g = max(0, issued - S::kStages); g < issued; ++g) {
                 const long long t0 = clock64();
                 while (!mbar_test(&full[g % S::kStages], (g / S::kStages) & 1) && clock64() - t0 < kSpinLimit) {
@@ -388,13 +448,16 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 }
                 tc_commit_elect(&s_full[t]);
             };
-            auto pv = [&](int t, int s, bool first) {
+            // half 0 and 1: keys 0-63 and 64-127 of the tile
+            auto pv = [&](int t, int s, int half, bool first) {
                 const uint64_t b = n_major_desc(saddr(kv_s) + s * S::kTileBytes);
 #pragma unroll
-                for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                    tc_mma_bf16_ts_elect(base + 256 + t * 128, base + t * 128 + kk * 8, b + (uint64_t)(kk * (2048 >> 4)), kPv,
-                                         first && kk == 0 ? 0u : 1u);
-                tc_commit_elect(&o_done[t]);
+                for (int k4 = 0; k4 < kTileKeys / 32; ++k4) {
+                    const int kk = half * (kTileKeys / 32) + k4;
+                    tc_mma_bf16_ts_elect(base + 256 + t * 128, base + t * 128 + kk * 8, b + (uint64_t)(kk * (2048 >> 4)),
+                                         kPv, first && kk == 0 ? 0u : 1u);
+                }
+                if (half) tc_commit_elect(&o_done[t]);
             };
             if (ok) ok = mbar_wait_warp(&full[0], 0, abort_flag);
             if (ok) {
@@ -407,10 +470,13 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 ok = mbar_wait_warp(&full[sv], (gv / S::kStages) & 1, abort_flag);
                 if (ok && j + 1 < n) ok = mbar_wait_warp(&full[sk], (gk / S::kStages) & 1, abort_flag);
                 for (int t = 0; ok && t < tiles; ++t) {
-                    ok = mbar_wait_warp(&p_ready[t], j & 1, abort_flag);
+                    for (int half = 0; ok && half < 2; ++half) {
+                        ok = mbar_wait_warp(&p_ready[2 * t + half], j & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(t, sv, half, j == 0);
+                    }
                     if (!ok) break;
-                    tc_fence_after();
-                    pv(t, sv, j == 0);
                     if (t == tiles - 1) tc_commit_elect(&empty[sv]);
                     if (j + 1 < n) {
                         qk(t, sk);
@@ -433,16 +499,17 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     }
 }
 
-// [batch, heads, tokens, dh] by strides, in boxes of one chunk by 64 elements.
+// [batch, heads, tokens, dh] by strides, in boxes of `box` tokens by 64 elements.
 // An axis that repeats one row (stride 0) has size 1 in the map; bits 0 and 1 of
 // `axes` say whether the head and the batch entry are coordinates.
-bool tensor_map(const Masked &p, const void *x, const int64_t (&stride)[3], CUtensorMap *map, int *axes) {
+bool tensor_map(const Masked &p, const void *x, int tokens, int heads, const int64_t (&stride)[3], int box_tokens,
+                CUtensorMap *map, int *axes) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    const int sizes[2] = {p.c.kv_heads, p.c.batch};
-    cuuint64_t dims[4] = {(cuuint64_t)p.c.dh, (cuuint64_t)p.c.nk_tokens, 1, 1}, bytes[3];
+    const int sizes[2] = {heads, p.c.batch};
+    cuuint64_t dims[4] = {(cuuint64_t)p.c.dh, (cuuint64_t)tokens, 1, 1}, bytes[3];
     const cuuint64_t row = (cuuint64_t)p.c.dh * 2;
-    bytes[0] = p.c.nk_tokens > 1 ? (cuuint64_t)stride[2] * 2 : row;
+    bytes[0] = tokens > 1 ? (cuuint64_t)stride[2] * 2 : row;
     *axes = 0;
     for (int i = 0; i < 2; ++i) {
         const int64_t st = stride[1 - i];
@@ -453,21 +520,21 @@ bool tensor_map(const Masked &p, const void *x, const int64_t (&stride)[3], CUte
             *axes |= 1 << i;
         }
     }
-    const cuuint32_t box[4] = {64u, (cuuint32_t)p.c.chunk, 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t box[4] = {64u, (cuuint32_t)box_tokens, 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
     return enc(map, p.c.dtype == RR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                const_cast<void *>(x), dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Units that fill a tile of 128 rows; keys whose tokens are apart (a map has no
-// stride of 0 there) and within the map's strides.
+// Units that fill a tile of 128 rows; operands whose tokens are apart (a map has
+// no stride of 0 there) and within the map's strides.
 bool tc_takes(const Masked &p) {
     if ((p.group << p.shift) < kTileRows || p.c.nk_tokens < 1 || p.c.width < 1) return false;
-    for (const int64_t (*s)[3] : {&p.c.k_stride, &p.c.v_stride}) {
-        if (p.c.nk_tokens > 1 && (*s)[2] == 0) return false;
+    if (p.c.nk_tokens > 1 && (p.c.k_stride[2] == 0 || p.c.v_stride[2] == 0)) return false;
+    if (p.c.nq_tokens > 1 && p.c.q_stride[2] == 0) return false;
+    for (const int64_t (*s)[3] : {&p.c.q_stride, &p.c.k_stride, &p.c.v_stride, &p.c.out_stride})
         for (int64_t x : *s)
             if (x >= 1ll << 39) return false;
-    }
     return true;
 }
 
@@ -475,16 +542,20 @@ template <typename T, int DH>
 cudaError_t launch_tc_as(const Masked &p, unsigned units, cudaStream_t s) {
     using S = TcShape<DH>;
     static_assert(S::kSmem <= 232448, "shared memory of one CTA");
-    CUtensorMap map_k, map_v;
-    int k_axes, v_axes;
-    if (!tensor_map(p, p.a.k, p.c.k_stride, &map_k, &k_axes) || !tensor_map(p, p.a.v, p.c.v_stride, &map_v, &v_axes))
+    Maps maps;
+    const rr_masked_attn_config &c = p.c;
+    if (!tensor_map(p, p.a.q, c.nq_tokens, c.q_heads, c.q_stride, c.chunk, &maps.q, &maps.axes[0]) ||
+        !tensor_map(p, p.a.k, c.nk_tokens, c.kv_heads, c.k_stride, c.chunk, &maps.k, &maps.axes[1]) ||
+        !tensor_map(p, p.a.v, c.nk_tokens, c.kv_heads, c.v_stride, c.chunk, &maps.v, &maps.axes[2]) ||
+        !tensor_map(p, p.a.out, c.nq_tokens, c.q_heads, c.out_stride, c.chunk < 32 ? c.chunk : 32, &maps.out,
+                    &maps.axes[3]))
         return cudaErrorInvalidValue;
     auto kern = masked_attention_tc_kernel<T, DH>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     Masked q = p;
     q.tiles = ((p.group << p.shift) + kTiles * kTileRows - 1) / (kTiles * kTileRows);
-    kern<<<units * (unsigned)q.tiles, kTcThreads, S::kSmem, s>>>(q, map_k, map_v, k_axes, v_axes);
+    kern<<<units * (unsigned)q.tiles, kTcThreads, S::kSmem, s>>>(q, maps);
     return cudaGetLastError();
 }
 
