@@ -35,8 +35,8 @@ constexpr int kTiles = 2;
 constexpr int kSoftWarps = 4 * kTiles;
 constexpr int kTcThreads = 32 * (kSoftWarps + 4);   // two warps of the last group are idle
 // Registers: launched with 168 a thread (384 threads: 64512 in all), then the two
-// softmax groups take 208 and the third keeps 88: 2 * 128 * 208 + 128 * 88 = 64512.
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
+// softmax groups take 224 and the third keeps 56: 2 * 128 * 224 + 128 * 56 = 64512.
+constexpr int kSoftRegs = 224, kOtherRegs = 56;
 constexpr float kSlack = 8.f;     // growth of the maximum that is let pass
 constexpr float kLift = 7.f;      // weights are 2^7 at the maximum
 constexpr int kSubBytes = kTileRows * 128;    // 128 rows of 64 elements
@@ -202,8 +202,8 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             const bool docs = p.a.doc_q != nullptr, bias = p.a.slopes != nullptr, cap = p.c.soft_cap > 0.f;
             const int doc = docs && valid ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + token] : -1;
             const int32_t *doc_k = docs ? p.a.doc_k + (size_t)u.b * p.c.nk_tokens : nullptr;
-            // keys below this are in sight
-            const int limit = min(p.c.nk_tokens, p.c.causal ? max(pos + 1, u.prefix) : p.c.nk_tokens);
+            // keys below this are in sight; none to a row without a document
+            const int limit = docs && doc < 0 ? 0 : min(p.c.nk_tokens, p.c.causal ? max(pos + 1, u.prefix) : p.c.nk_tokens);
             const float slope = bias ? p.a.slopes[head] * kLog2e : 0.f;
             int near = 0;
             if (bias) {
@@ -215,6 +215,19 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < n; ++j) {
+                // what the tile's chunks are to the unit: lane e looks at chunk e; lane i
+                // fetches the documents of keys 4i .. 4i + 3 while S is computed
+                const int per = kTileKeys >> p.shift;
+                const int mine = j * per + lane < n_list ? s_list[j * per + lane] : -1;
+                const bool plain = __all_sync(kFull, lane >= per || (mine >= 0 && (mine & kChunkFull)));
+                int dk[4];
+                if (docs && !plain) {
+                    const int entry = __shfl_sync(kFull, mine, (4 * lane) >> p.shift);
+                    const int at = ((entry & kChunkId) << p.shift) + ((4 * lane) & (p.c.chunk - 1));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        dk[c] = entry >= 0 && at + c < p.c.nk_tokens ? doc_k[at + c] : -1;
+                }
                 ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
@@ -240,10 +253,6 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     }
                 }
                 const float scale = cap ? 1.f : p.s1;
-                // what a tile's chunks are to the unit: lane e looks at chunk e of the tile
-                const int per = kTileKeys >> p.shift;
-                const int mine = j * per + lane < n_list ? s_list[j * per + lane] : -1;
-                const bool plain = __all_sync(kFull, lane >= per || (mine >= 0 && (mine & kChunkFull)));
                 if (bias) {
 #pragma unroll
                     for (int c0 = 0; c0 < kTileKeys; c0 += 16) {
@@ -261,16 +270,13 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         if (entry >= 0 && (entry & kChunkFull)) continue;
                         const int base = entry < 0 ? 0 : ((entry & kChunkId) << p.shift) + (c0 & (p.c.chunk - 1));
                         const int left = entry < 0 ? 0 : limit - base;
-                        if (docs) {
-                            int dk[16];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) dk[c] = doc_k[min(base + c, p.c.nk_tokens - 1)];
+                        for (int c = 0; c < 16; ++c) s[c0 + c] = c < left ? s[c0 + c] : -INFINITY;
+                    }
+                    if (docs) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) s[c0 + c] = c < left && dk[c] == doc && doc >= 0 ? s[c0 + c] : -INFINITY;
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) s[c0 + c] = c < left ? s[c0 + c] : -INFINITY;
-                        }
+                        for (int c = 0; c < kTileKeys; ++c)
+                            if (__shfl_sync(kFull, dk[c & 3], c >> 2) != doc) s[c] = -INFINITY;
                     }
                 }
                 const float mul = bias ? 1.f : scale;
