@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -122,23 +123,20 @@ def _load():
     lib.rr_route_layer_static.restype = ctypes.c_int
     lib.rr_sparse_attention.argtypes = [ctypes.POINTER(rr_attn_config), P, P, P, P, P, P]
     lib.rr_sparse_attention.restype = ctypes.c_int
-    ref = ctypes.POINTER
-    lib.rr_masked_attention.argtypes = [ref(rr_masked_attn_config), ref(rr_masked_attn_args), P]
+    # structures of the calls below go as addresses of packed bytes
+    lib.rr_masked_attention.argtypes = [P, P, P]
     lib.rr_masked_attention.restype = ctypes.c_int
     for name in ("rr_cache_codes_bytes", "rr_cache_scales_bytes"):
         f = getattr(lib, name)
-        f.argtypes = [ref(rr_cache_config)]
+        f.argtypes = [P]
         f.restype = ctypes.c_size_t
     for name in ("rr_cache_write", "rr_cache_read"):
         f = getattr(lib, name)
-        f.argtypes = [ref(rr_cache_config), ref(rr_cache_pool), ref(rr_cache_rows), P, ctypes.c_int64 * 2, P,
-                      ctypes.c_int64 * 2, ctypes.c_int32, P]
+        f.argtypes = [P, P, P, P, P, P, P, ctypes.c_int32, P]
         f.restype = ctypes.c_int
-    lib.rr_cached_attention_workspace_bytes.argtypes = [ref(rr_cache_config), ref(rr_cached_attn_config),
-                                                        ctypes.c_int32]
+    lib.rr_cached_attention_workspace_bytes.argtypes = [P, P, ctypes.c_int32]
     lib.rr_cached_attention_workspace_bytes.restype = ctypes.c_size_t
-    lib.rr_cached_attention.argtypes = [ref(rr_cache_config), ref(rr_cache_pool), ref(rr_cached_attn_config),
-                                        ref(rr_cached_attn_args), P, ctypes.c_size_t, P]
+    lib.rr_cached_attention.argtypes = [P, P, P, P, P, ctypes.c_size_t, P]
     lib.rr_cached_attention.restype = ctypes.c_int
     lib.rr_status_string.argtypes = [ctypes.c_int]
     lib.rr_status_string.restype = ctypes.c_char_p
@@ -254,42 +252,42 @@ def rr_sparse_attention(cfg: rr_attn_config, d_q: int, d_k: int, d_v: int, d_rou
 
 def rr_masked_attention(cfg: rr_masked_attn_config, args: rr_masked_attn_args, stream: int) -> None:
     """Masked attention over a route (include/rr_attention.h)."""
-    _check(_lib.rr_masked_attention(cfg, args, stream), "rr_masked_attention")
+    _check(_lib.rr_masked_attention(ctypes.byref(cfg), ctypes.byref(args), stream), "rr_masked_attention")
 
 
 def rr_cache_codes_bytes(cfg: rr_cache_config) -> int:
-    return int(_lib.rr_cache_codes_bytes(cfg))
+    return int(_lib.rr_cache_codes_bytes(ctypes.byref(cfg)))
 
 
 def rr_cache_scales_bytes(cfg: rr_cache_config) -> int:
-    return int(_lib.rr_cache_scales_bytes(cfg))
+    return int(_lib.rr_cache_scales_bytes(ctypes.byref(cfg)))
 
 
 def rr_cache_write(cfg: rr_cache_config, pool: rr_cache_pool, rows: rr_cache_rows, d_k: int, k_stride, d_v: int,
                    v_stride, dtype: int, stream: int) -> None:
     """Quantised store into the paged cache (include/rr_cache.h)."""
     pair = ctypes.c_int64 * 2
-    _check(_lib.rr_cache_write(cfg, pool, rows, d_k, pair(*k_stride), d_v, pair(*v_stride), dtype, stream),
-           "rr_cache_write")
+    _check(_lib.rr_cache_write(ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(rows), d_k, pair(*k_stride), d_v,
+                               pair(*v_stride), dtype, stream), "rr_cache_write")
 
 
 def rr_cache_read(cfg: rr_cache_config, pool: rr_cache_pool, rows: rr_cache_rows, d_k: int, k_stride, d_v: int,
                   v_stride, dtype: int, stream: int) -> None:
     """Rows of the paged cache read back (include/rr_cache.h)."""
     pair = ctypes.c_int64 * 2
-    _check(_lib.rr_cache_read(cfg, pool, rows, d_k, pair(*k_stride), d_v, pair(*v_stride), dtype, stream),
-           "rr_cache_read")
+    _check(_lib.rr_cache_read(ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(rows), d_k, pair(*k_stride), d_v,
+                              pair(*v_stride), dtype, stream), "rr_cache_read")
 
 
 def rr_cached_attention_workspace_bytes(cfg: rr_cache_config, attn: rr_cached_attn_config, routed: bool) -> int:
-    return int(_lib.rr_cached_attention_workspace_bytes(cfg, attn, int(bool(routed))))
+    return int(_lib.rr_cached_attention_workspace_bytes(ctypes.byref(cfg), ctypes.byref(attn), int(bool(routed))))
 
 
 def rr_cached_attention(cfg: rr_cache_config, pool: rr_cache_pool, attn: rr_cached_attn_config,
                         args: rr_cached_attn_args, workspace: int, workspace_bytes: int, stream: int) -> None:
     """Attention over the paged cache (include/rr_cache.h)."""
-    _check(_lib.rr_cached_attention(cfg, pool, attn, args, workspace, workspace_bytes, stream),
-           "rr_cached_attention")
+    _check(_lib.rr_cached_attention(ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(attn), ctypes.byref(args),
+                                    workspace, workspace_bytes, stream), "rr_cached_attention")
 
 
 # ---- convenience wrapper over torch memory --------------------------------
@@ -378,49 +376,61 @@ def _describe(t) -> str:
     return f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
 
 
-class _call_on:
-    """The device and stream of a call: makes the tensors' device current and,
-    where the caller names a stream, that stream too, so that what the call
-    allocates belongs to it.  Yields the stream's handle."""
-
-    def __init__(self, device, stream):
-        self.context = None
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device) if stream \
-                    else torch.cuda.default_stream(device)
-            if stream.device != device:
-                raise ValueError(f"stream: expected a stream of {device}, got one of {stream.device}")
-            self.context = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.context = torch.cuda.device(device)
-        self.device = device
-
-    def __enter__(self) -> int:
-        if self.context is not None:
-            self.context.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *error):
-        if self.context is not None:
-            self.context.__exit__(*error)
+# The structures of include/rr_attention.h and rr_cache.h as struct formats: a call
+# packs them in one step, a third of the time that filling ctypes fields takes.
+_MASKED_CFG, _MASKED_ARGS = struct.Struct("@13i2f12q"), struct.Struct("@10P")
+_CACHE_CFG, _CACHE_POOL, _CACHE_ROWS = struct.Struct("@5i"), struct.Struct("@2P"), struct.Struct("@2i3P2i")
+_CACHED_CFG, _CACHED_ARGS, _TWO = struct.Struct("@8i2f3q"), struct.Struct("@7P"), struct.Struct("@2q")
+for _fmt, _structure in ((_MASKED_CFG, rr_masked_attn_config), (_MASKED_ARGS, rr_masked_attn_args),
+                         (_CACHE_CFG, rr_cache_config), (_CACHE_POOL, rr_cache_pool), (_CACHE_ROWS, rr_cache_rows),
+                         (_CACHED_CFG, rr_cached_attn_config), (_CACHED_ARGS, rr_cached_attn_args)):
+    assert _fmt.size == ctypes.sizeof(_structure), _structure
 
 
-def _int32(name, t, shape, device):
-    """A contiguous int32 tensor of this shape (None: any size there)."""
-    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) or not t.is_contiguous() \
-            or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected contiguous int32 {shape} on {device}, got {_describe(t)}")
+def _on_stream(index: int, stream, call, *args):
+    """call(stream handle, *args) with CUDA device `index` current and, where the
+    caller names a stream, that stream too, so that what the call allocates
+    belongs to it."""
+    if stream is None:
+        if torch._C._cuda_getDevice() == index:
+            return call(torch._C._cuda_getCurrentRawStream(index), *args)
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index), *args)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream: expected a stream of cuda:{index}, got one of {stream.device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream, *args)
+
+
+def _int32(name, t, shape, index):
+    """Address of a contiguous int32 tensor of this shape (None: any size there)."""
+    got = t.shape
+    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous() or len(got) != len(shape) \
+            or (got != shape and any(n is not None and n != m for n, m in zip(shape, got))):
+        raise ValueError(f"{name}: expected contiguous int32 {shape} on cuda:{index}, got {_describe(t)}")
     return t.data_ptr()
 
 
-def _slopes(t, heads, device):
+def _slopes(t, heads, index):
     if t is None:
-        return None
-    if t.dtype != torch.float32 or t.device != device or t.dim() != 1 or t.shape[0] != heads \
-            or not t.is_contiguous():
-        raise ValueError(f"slopes: expected contiguous float32 [{heads}] on {device}, got {_describe(t)}")
+        return 0
+    if t.dtype is not torch.float32 or t.get_device() != index or t.shape != (heads,) or not t.is_contiguous():
+        raise ValueError(f"slopes: expected contiguous float32 [{heads}] on cuda:{index}, got {_describe(t)}")
     return t.data_ptr()
+
+
+def _rows_like(name, t, dtype, shape, index):
+    """Strides, all but the last, of a tensor of this type and shape whose rows
+    are contiguous; that of a size of one counts nothing."""
+    st = t.stride()
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or st[-1] != 1:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{index}, the last dimension contiguous, "
+                         f"got {_describe(t)}")
+    if 1 in shape:
+        return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], st))
+    return st[:-1]
 
 
 def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: torch.Tensor, chunk: int,
@@ -440,72 +450,61 @@ def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: t
     stride] of key-chunk ids, of which the first `width` (default: all) are
     read.  q_offset: position of query token 0.  Returns (or fills) `out` like
     q, with return_lse also the float32 [batch, q_heads, nq_tokens] logarithms
-    of the softmax sums."""
-    device, dtype = q.device, q.dtype
-    if q.dim() != 4 or k.dim() != 4 or dtype not in _HALVES or not q.is_cuda:
+    of the softmax sums.  With a `stream`, the results belong to it."""
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    if len(shape) != 4 or k.dim() != 4 or dtype not in _HALVES or index < 0:
         raise ValueError(f"q: expected bf16 or f16 [batch, heads, tokens, dh] on a CUDA device, got {_describe(q)}")
-    batch, q_heads, nq, dh = q.shape
+    batch, q_heads, nq, dh = shape
     kv_heads, nk = k.shape[1], k.shape[2]
-    for name, t in (("k", k), ("v", v)):
-        if t.dtype != dtype or t.device != device or t.shape != (batch, kv_heads, nk, dh) or t.stride(3) != 1:
-            raise ValueError(f"{name}: expected {dtype} {(batch, kv_heads, nk, dh)} on {device}, dh contiguous, "
-                             f"got {_describe(t)}")
-    if q.stride(3) != 1:
-        raise ValueError(f"q: expected dh contiguous, got {_describe(q)}")
-    chunks = -(-nq // chunk) if chunk > 0 else 0
-    d_route = _int32("route", route, (batch, None, chunks, None), device)
+    kv_shape = (batch, kv_heads, nk, dh)
+    strides = _rows_like("q", q, dtype, shape, index) + _rows_like("k", k, dtype, kv_shape, index) \
+        + _rows_like("v", v, dtype, kv_shape, index)
+    d_route = _int32("route", route, (batch, None, -(-nq // chunk) if chunk > 0 else 0, None), index)
     route_heads, stride = route.shape[1], route.shape[3]
     width = stride if width is None else int(width)
     if width > stride:
         raise ValueError(f"width {width} is larger than the route's {stride} entries")
-    if out is not None and (out.dtype != dtype or out.device != device or out.shape != q.shape
-                            or out.stride(3) != 1):
-        raise ValueError(f"out: expected {dtype} {tuple(q.shape)} on {device}, dh contiguous, got {_describe(out)}")
     if (doc_q is None) != (doc_k is None):
         raise ValueError("doc_q and doc_k go together")
-    d_slopes = _slopes(slopes, q_heads, device)
-    d_doc_q = None if doc_q is None else _int32("doc_q", doc_q, (batch, nq), device)
-    d_doc_k = None if doc_k is None else _int32("doc_k", doc_k, (batch, nk), device)
-    d_prefix = None if prefix is None else _int32("prefix", prefix, (batch,), device)
-    with _call_on(device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q)
-        lse = torch.empty((batch, q_heads, nq), dtype=torch.float32, device=device) if return_lse else None
-        ints = ctypes.c_int64 * 3
-        cfg = rr_masked_attn_config(batch, q_heads, kv_heads, route_heads, nq, nk, dh, chunk, width, max(stride, 1),
-                                    int(bool(causal)), _DTYPES[dtype], q_offset, 0.0 if scale is None else scale,
-                                    soft_cap, ints(*_strides(q)), ints(*_strides(k)), ints(*_strides(v)),
-                                    ints(*_strides(out)))
-        args = rr_masked_attn_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), d_route, d_slopes, d_doc_q, d_doc_k,
-                                   d_prefix, out.data_ptr(), None if lse is None else lse.data_ptr())
-        rr_masked_attention(cfg, args, handle)
+    ints = (batch, q_heads, kv_heads, route_heads, nq, nk, dh, chunk, width, max(stride, 1), 1 if causal else 0,
+            _DTYPES[dtype], q_offset, 0.0 if scale is None else scale, soft_cap) + strides
+    ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), d_route, _slopes(slopes, q_heads, index),
+            0 if doc_q is None else _int32("doc_q", doc_q, (batch, nq), index),
+            0 if doc_k is None else _int32("doc_k", doc_k, (batch, nk), index),
+            0 if prefix is None else _int32("prefix", prefix, (batch,), index))
+    return _on_stream(index, stream, _masked_attention, q, out, return_lse, ints, ptrs)
+
+
+def _masked_attention(handle, q, out, return_lse, ints, ptrs):
+    if out is None:
+        out = torch.empty_like(q)
+    out_strides = _rows_like("out", out, q.dtype, q.shape, q.get_device())
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    _check(_lib.rr_masked_attention(_MASKED_CFG.pack(*ints, *out_strides),
+                                    _MASKED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),
+                                    handle), "rr_masked_attention")
     return (out, lse) if return_lse else out
 
 
-def _strides(t):
-    """Strides of all but the last dimension; that of a size of one counts nothing."""
-    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride())]
-
-
 def _cache(codes, scales, dh):
-    """(config, pool) of a cache's two arrays, for rows of dh elements."""
-    device = codes.device
-    if codes.dtype != torch.uint8 or not codes.is_cuda or codes.dim() != 5 or codes.shape[2] != 2 \
-            or not codes.is_contiguous():
+    """(config, pool, device index, heads) of a cache's two arrays, for rows of dh elements."""
+    index, shape = codes.get_device(), codes.shape
+    if codes.dtype is not torch.uint8 or index < 0 or len(shape) != 5 or shape[2] != 2 or not codes.is_contiguous():
         raise ValueError(f"codes: expected contiguous uint8 [pages, heads, 2, chunk, bytes] on a CUDA device, "
                          f"got {_describe(codes)}")
-    pages, heads, _, chunk, row = codes.shape
+    pages, heads, _, chunk, row = shape
     if row == dh:
         fmt, groups = RR_E4M3, 1
     elif 2 * row == dh:
         fmt, groups = RR_E2M1, dh // 32
     else:
         raise ValueError(f"codes: rows of {row} bytes hold no {dh} elements (e4m3: {dh} bytes, e2m1: {dh // 2})")
-    if scales.dtype != torch.uint8 or scales.device != device or scales.shape != (pages, heads, 2, chunk, groups) \
-            or not scales.is_contiguous():
-        raise ValueError(f"scales: expected contiguous uint8 {(pages, heads, 2, chunk, groups)} on {device}, "
+    if scales.dtype is not torch.uint8 or scales.get_device() != index or not scales.is_contiguous() \
+            or scales.shape != (pages, heads, 2, chunk, groups):
+        raise ValueError(f"scales: expected contiguous uint8 {(pages, heads, 2, chunk, groups)} on cuda:{index}, "
                          f"got {_describe(scales)}")
-    return rr_cache_config(pages, heads, dh, chunk, fmt), rr_cache_pool(codes.data_ptr(), scales.data_ptr())
+    return _CACHE_CFG.pack(pages, heads, dh, chunk, fmt), _CACHE_POOL.pack(codes.data_ptr(), scales.data_ptr()), \
+        index, heads
 
 
 def cache_empty(pages: int, heads: int, chunk: int, dh: int, fmt: str = "e4m3", device=None):
@@ -513,18 +512,18 @@ def cache_empty(pages: int, heads: int, chunk: int, dh: int, fmt: str = "e4m3", 
     (every row reads as zeros); fmt "e4m3" or "e2m1"."""
     if fmt not in ("e4m3", "e2m1"):
         raise ValueError(f'fmt: expected "e4m3" or "e2m1", got {fmt!r}')
-    if pages < 0 or heads < 1 or chunk not in (16, 32, 64, 128) or dh not in (64, 128):
+    if rr_cache_scales_bytes(rr_cache_config(1, heads, dh, chunk, RR_E4M3)) == 0 or pages < 0:
         raise RRError(RR_EINVAL, f"cache_empty(pages={pages}, heads={heads}, chunk={chunk}, dh={dh})")
     row, groups = (dh, 1) if fmt == "e4m3" else (dh // 2, dh // 32)
     mk = lambda n: torch.zeros((pages, heads, 2, chunk, n), dtype=torch.uint8, device=device or "cuda")
     return mk(row), mk(groups)
 
 
-def _rows(rows, cu, start, table, device):
-    d_table = _int32("table", table, (None, None), device)
+def _ragged(rows, cu, start, table, index):
+    d_table = _int32("table", table, (None, None), index)
     batch, width = table.shape
-    return rr_cache_rows(batch, rows, _int32("cu", cu, (batch + 1,), device),
-                         _int32("start", start, (batch,), device), d_table, width, max(width, 1))
+    return _CACHE_ROWS.pack(batch, rows, _int32("cu", cu, (batch + 1,), index),
+                            _int32("start", start, (batch,), index), d_table, width, max(width, 1))
 
 
 def cache_write(codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
@@ -535,18 +534,19 @@ def cache_write(codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor, v: t
     heads, dh] of one type (f32, bf16, f16), any strides that keep rows 16-byte
     aligned; rows cu[b]..cu[b+1]-1 are sequence b's at positions start[b]...;
     table [batch, width]: pages of each sequence's chunks (-1: none)."""
-    device, dtype = codes.device, k.dtype
-    if k.dim() != 3 or dtype not in _DTYPES:
+    dtype, shape = k.dtype, k.shape
+    if len(shape) != 3 or dtype not in _DTYPES:
         raise ValueError(f"k: expected f32, bf16 or f16 [rows, heads, dh], got {_describe(k)}")
-    rows, heads, dh = k.shape
-    cfg, pool = _cache(codes, scales, dh)
-    for name, t in (("k", k), ("v", v)):
-        if t.dtype != dtype or t.device != device or t.shape != (rows, cfg.heads, dh) or t.stride(2) != 1:
-            raise ValueError(f"{name}: expected {dtype} {(rows, cfg.heads, dh)} on {device}, dh contiguous, "
-                             f"got {_describe(t)}")
-    batch = _rows(rows, cu, start, table, device)
-    with _call_on(device, stream) as handle:
-        rr_cache_write(cfg, pool, batch, k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), _DTYPES[dtype], handle)
+    cfg, pool, index, heads = _cache(codes, scales, shape[2])
+    want = (shape[0], heads, shape[2])
+    args = (cfg, pool, _ragged(shape[0], cu, start, table, index), k.data_ptr(),
+            _TWO.pack(*_rows_like("k", k, dtype, want, index)), v.data_ptr(),
+            _TWO.pack(*_rows_like("v", v, dtype, want, index)), _DTYPES[dtype])
+    _on_stream(index, stream, _cache_write, args)
+
+
+def _cache_write(handle, args):
+    _check(_lib.rr_cache_write(*args, handle), "rr_cache_write")
 
 
 def cache_read(codes: torch.Tensor, scales: torch.Tensor, cu: torch.Tensor, start: torch.Tensor,
@@ -556,18 +556,21 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, cu: torch.Tensor, star
     dh] of `dtype`; see cache_write for the arguments.  Rows that belong to no
     sequence are not written: they keep what `out` (a pair of tensors to fill)
     held, and are unspecified without it."""
-    device = codes.device
-    cfg, pool = _cache(codes, scales, dh)
+    cfg, pool, index, heads = _cache(codes, scales, dh)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype: expected float32, bfloat16 or float16, got {dtype}")
-    shape = (rows, cfg.heads, dh)
-    batch = _rows(rows, cu, start, table, device)
-    for name, t in zip("kv", out or ()):
-        if t.dtype != dtype or t.device != device or t.shape != shape or t.stride(2) != 1:
-            raise ValueError(f"out {name}: expected {dtype} {shape} on {device}, dh contiguous, got {_describe(t)}")
-    with _call_on(device, stream) as handle:
-        k, v = out if out is not None else (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
-        rr_cache_read(cfg, pool, batch, k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), _DTYPES[dtype], handle)
+    if rows < 0:
+        raise ValueError(f"rows: expected 0 or more, got {rows}")
+    args = (cfg, pool, _ragged(rows, cu, start, table, index))
+    return _on_stream(index, stream, _cache_read, args, out, (rows, heads, dh), dtype, codes.device, index)
+
+
+def _cache_read(handle, args, out, shape, dtype, device, index):
+    k, v = out if out is not None else (torch.empty(shape, dtype=dtype, device=device),
+                                        torch.empty(shape, dtype=dtype, device=device))
+    _check(_lib.rr_cache_read(*args, k.data_ptr(), _TWO.pack(*_rows_like("out k", k, dtype, shape, index)),
+                              v.data_ptr(), _TWO.pack(*_rows_like("out v", v, dtype, shape, index)), _DTYPES[dtype],
+                              handle), "rr_cache_read")
     return k, v
 
 
@@ -584,46 +587,49 @@ def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
     are read.  Returns (or fills) out like q, contiguous, with return_lse also
     float32 [batch, q_tokens, q_heads].  `workspace`: uint8 device memory of
     rr_cached_attention_workspace_bytes, for callers that hold their own; two
-    calls that can run at once need one each."""
-    device, dtype = codes.device, q.dtype
-    if q.dim() != 4 or dtype not in _HALVES or q.device != device or q.stride(3) != 1:
-        raise ValueError(f"q: expected bf16 or f16 [batch, tokens, heads, dh] on {device}, dh contiguous, "
-                         f"got {_describe(q)}")
-    batch, q_tokens, q_heads, dh = q.shape
-    cfg, pool = _cache(codes, scales, dh)
-    d_table = _int32("table", table, (batch, None), device)
-    stride = 1
-    d_route = None
-    if route is not None:
-        d_route = _int32("route", route, (batch, cfg.heads, None), device)
-        stride = route.shape[2]
-    width = (stride if route is not None else 0) if width is None else int(width)
-    if route is None and width:
-        raise ValueError("width goes with a route")
-    if width > stride:
-        raise ValueError(f"width {width} is larger than the route's {stride} entries")
-    if out is not None and (out.dtype != dtype or out.device != device or out.shape != q.shape
-                            or not out.is_contiguous()):
-        raise ValueError(f"out: expected contiguous {dtype} {tuple(q.shape)} on {device}, got {_describe(out)}")
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != device
-                                  or not workspace.is_contiguous()):
-        raise ValueError(f"workspace: expected contiguous uint8 on {device}, got {_describe(workspace)}")
+    calls that can run at once need one each.  With a `stream`, the results
+    belong to it."""
+    dtype, shape = q.dtype, q.shape
+    if len(shape) != 4 or dtype not in _HALVES:
+        raise ValueError(f"q: expected bf16 or f16 [batch, tokens, heads, dh], got {_describe(q)}")
+    batch, q_tokens, q_heads, dh = shape
+    cfg, pool, index, heads = _cache(codes, scales, dh)
+    q_strides = _rows_like("q", q, dtype, shape, index)
+    d_table = _int32("table", table, (batch, None), index)
     table_width = table.shape[1]
-    attn = rr_cached_attn_config(batch, q_tokens, q_heads, _DTYPES[dtype], table_width, max(table_width, 1), width,
-                                 max(stride, 1), 0.0 if scale is None else scale, soft_cap,
-                                 (ctypes.c_int64 * 3)(*_strides(q)))
-    d_lens, d_slopes = _int32("seq_lens", seq_lens, (batch,), device), _slopes(slopes, q_heads, device)
-    need = rr_cached_attention_workspace_bytes(cfg, attn, route is not None)
-    with _call_on(device, stream) as handle:
-        if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=device)
-        lse = torch.empty((batch, q_tokens, q_heads), dtype=torch.float32, device=device) if return_lse else None
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        args = rr_cached_attn_args(q.data_ptr(), d_lens, d_table, d_route, d_slopes, out.data_ptr(),
-                                   None if lse is None else lse.data_ptr())
-        rr_cached_attention(cfg, pool, attn, args, None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.numel(), handle)
+    stride, d_route = 1, 0
+    if route is not None:
+        d_route = _int32("route", route, (batch, heads, None), index)
+        stride = route.shape[2]
+        width = stride if width is None else int(width)
+        if width > stride:
+            raise ValueError(f"width {width} is larger than the route's {stride} entries")
+    elif width:
+        raise ValueError("width goes with a route")
+    if out is not None and (_rows_like("out", out, dtype, shape, index) is None or not out.is_contiguous()):
+        raise ValueError(f"out: expected contiguous {dtype} {tuple(shape)} on cuda:{index}, got {_describe(out)}")
+    if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.get_device() != index
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected contiguous uint8 on cuda:{index}, got {_describe(workspace)}")
+    attn = _CACHED_CFG.pack(batch, q_tokens, q_heads, _DTYPES[dtype], table_width, max(table_width, 1), width or 0,
+                            max(stride, 1), 0.0 if scale is None else scale, soft_cap, *q_strides)
+    ptrs = (q.data_ptr(), _int32("seq_lens", seq_lens, (batch,), index), d_table, d_route,
+            _slopes(slopes, q_heads, index))
+    return _on_stream(index, stream, _cached_attention, q, out, return_lse, workspace, cfg, pool, attn, ptrs)
+
+
+def _cached_attention(handle, q, out, return_lse, workspace, cfg, pool, attn, ptrs):
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        need = _lib.rr_cached_attention_workspace_bytes(cfg, attn, 1 if ptrs[3] else 0)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    d_work, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _check(_lib.rr_cached_attention(cfg, pool, attn,
+                                    _CACHED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),
+                                    d_work, size, handle), "rr_cached_attention")
     return (out, lse) if return_lse else out
 
 

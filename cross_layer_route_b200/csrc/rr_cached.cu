@@ -859,7 +859,8 @@ cudaError_t launch(const Cached &p, cudaStream_t s) {
     const int smem = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 +
                      (ring > merge ? ring : merge);
     auto kern = cached_attention_kernel<FMT, DH, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), smem, done);
     if (e != cudaSuccess) return e;
     const dim3 grid(p.splits, p.n.batch * p.c.heads, (p.rows + 8 * NT - 1) / (8 * NT));
     kern<<<grid, 32 * kAttnWarps, smem, s>>>(p);

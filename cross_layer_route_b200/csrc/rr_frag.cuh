@@ -4,12 +4,28 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 namespace rr_attn {
 
 constexpr int kMaxWidth = 1024;     // route entries read per query chunk
 constexpr unsigned kFull = 0xffffffffu;
+
+// Lets a kernel have `bytes` of dynamic shared memory, on the current device, the
+// first time it is asked for there (`done`: a bit for each of 64 devices).
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -283,7 +283,8 @@ template <typename T, int DH>
 cudaError_t launch(const Masked &p, unsigned units, cudaStream_t s) {
     using S = Shape<DH>;
     auto kern = masked_attention_kernel<T, DH>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem, done);
     if (e != cudaSuccess) return e;
     const int warps = min(kMaxWarps, (p.group << p.shift) / 16);
     kern<<<units * (unsigned)p.tiles, 32 * warps, S::kSmem, s>>>(p);

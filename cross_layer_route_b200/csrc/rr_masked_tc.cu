@@ -557,7 +557,8 @@ cudaError_t launch_tc_as(const Masked &p, unsigned units, cudaStream_t s) {
                     &maps.axes[3]))
         return cudaErrorInvalidValue;
     auto kern = masked_attention_tc_kernel<T, DH>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem, done);
     if (e != cudaSuccess) return e;
     Masked q = p;
     q.tiles = ((p.group << p.shift) + kTiles * kTileRows - 1) / (kTiles * kTileRows);

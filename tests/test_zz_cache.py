@@ -372,7 +372,7 @@ def test_streams_graphs_and_workspaces(rr):
     got = [rr.cached_attention(codes, scales, q, *args, stream=s) for s in (side, side.cuda_stream)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got)
-    cfg, _ = rr._cache(codes, scales, 128)
+    cfg = rr.rr_cache_config(codes.shape[0], codes.shape[1], 128, codes.shape[3], rr.RR_E4M3)
     n = rr.rr_cached_attn_config(2, 1, 8, rr.RR_BF16, table.shape[1], table.shape[1], 0, 1)
     work = torch.empty(rr.rr_cached_attention_workspace_bytes(cfg, n, False), dtype=torch.uint8, device=DEV)
     assert work.numel() > 0
