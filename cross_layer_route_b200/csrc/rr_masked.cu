@@ -1,16 +1,20 @@
 // rr_masked.cu -- masked attention over a route (declared in
-// include/rr_attention.h): the entry point and the kernel on mma.sync.
+// include/rr_attention.h): the entry point and the kernel on mma.sync, for units
+// of fewer than 128 rows (rr_masked_tc.cu has the others).
 //
 // One CTA = up to 64 rows of a unit (rr_masked.cuh), 16 rows per warp, so the
 // query heads that share a key head read its chunks once.  Keys are visited in
-// tiles of 64 slots of the concatenated route (a tile holds several chunks of
-// 16 or 32, or half a chunk of 128), staged by cp.async two tiles deep into
-// rows padded by 16 bytes; slots past the route are filled with zeros and
-// masked.  S = q K^T, the softmax and O += P V as in rr_attention.cu, with
+// tiles of slots of the concatenated route (a tile holds several chunks, or a
+// part of one), staged by cp.async two tiles deep into rows padded by 16 bytes;
+// slots past the route are filled with zeros and masked.  S = q K^T and O += P V
+// on mma.sync with fp32 sums, P straight from the scores' registers, and
 //   x = s2 tanh(s1 s) or s1 s           (base-2 scores)
 //   x -= slope (|pos - key| - near)      near: the row's nearest visible key
-//   x = -inf where the masks say so, looked at per element only in tiles that
+//   x = -inf where the masks say so, looked at per element only in chunks that
 //       are not fully visible to the unit.
+// The running maximum moves only when a score passes it by 2^8 (weights are 2^7
+// at the maximum, which keeps small ones away from f16's subnormals), so most
+// tiles cost one vote and no rescaling.
 // A masked key has weight exactly zero; only a masked value row that holds an
 // infinity or a NaN could reach a result then, as 0 * NaN, and rows with such
 // accumulators are computed again on their own (row_alone).
@@ -22,46 +26,49 @@ namespace rr_masked {
 
 using namespace rr_attn;
 
-constexpr int kSlots = 64;      // key slots per tile
 constexpr int kMaxWarps = 4;    // 16 rows each
+constexpr float kSlack = 8.f;   // growth of the maximum that is let pass
+constexpr float kLift = 7.f;    // weights are 2^7 at the maximum
 
 template <int DH>
 struct Shape {
+    static constexpr int kSlots = 64;                           // key slots per tile
     static constexpr int kRow = DH + 8;
     static constexpr int kTile = kSlots * kRow;
-    static constexpr int kHead = kMaxWidth * 4 + 16;            // list and its length
-    static constexpr int kMeta = 2 * kSlots * 8;                // {position, document} per slot, two stages
-    static constexpr int kSmem = kHead + kMeta + 4 * kTile * 2;
+    static constexpr int kMeta = 2 * kSlots * 4;                // documents per slot, two stages
+    static constexpr int kSmem = kMeta + 4 * kTile * 2;         // and the list
+    static constexpr int kMinBlocks = 3;                         // CTAs per SM: at most 168 registers, no spills in the loop
 };
 
+// One tile of keys and values.  A thread copies the same 16-byte column of every
+// (blockDim / (DH / 8))-th slot.
 template <typename T, int DH>
 __device__ __forceinline__ void stage_tile(const Masked &p, const Unit &u, const int32_t *list, int slots, int tile,
-                                           const T *k, const T *v, T *sk, T *sv, int2 *meta) {
-    constexpr int kRow = Shape<DH>::kRow;
-    for (int idx = threadIdx.x; idx < kSlots * DH / 8; idx += blockDim.x) {
-        const int r = idx / (DH / 8), c = (idx % (DH / 8)) * 8;
-        const int slot = tile * kSlots + r;
-        int s = -1;
-        if (slot < slots) s = ((list[slot >> p.shift] & kChunkId) << p.shift) + (slot & (p.c.chunk - 1));
+                                           const T *k, const T *v, uint32_t sk, uint32_t sv, int32_t *meta) {
+    using S = Shape<DH>;
+    const int c = (threadIdx.x % (DH / 8)) * 8, step = blockDim.x / (DH / 8);
+    for (int r = threadIdx.x / (DH / 8); r < S::kSlots; r += step) {
+        const int slot = tile * S::kSlots + r;
+        int s = slot < slots ? ((list[slot >> p.shift] & kChunkId) << p.shift) + (slot & (p.c.chunk - 1)) : -1;
         if (s >= p.c.nk_tokens) s = -1;
-        const int64_t at = s < 0 ? 0 : s;
+        const int64_t at = max(s, 0);
         const int bytes = s < 0 ? 0 : 16;
-        cp_async16_zfill(smem_u32(sk + r * kRow + c), k + at * p.c.k_stride[2] + c, bytes);
-        cp_async16_zfill(smem_u32(sv + r * kRow + c), v + at * p.c.v_stride[2] + c, bytes);
-        if (c == 0)
-            meta[r] = make_int2(s, s >= 0 && p.a.doc_k ? p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] : 0);
+        const uint32_t to = (uint32_t)(r * S::kRow + c) * 2;
+        cp_async16_zfill(sk + to, k + at * p.c.k_stride[2] + c, bytes);
+        cp_async16_zfill(sv + to, v + at * p.c.v_stride[2] + c, bytes);
+        if (p.a.doc_k && c == 0) meta[r] = s >= 0 ? p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] : -1;
     }
 }
 
 template <typename T, int DH>
-__global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(const __grid_constant__ Masked p) {
+__global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_attention_kernel(const __grid_constant__ Masked p) {
     using S = Shape<DH>;
+    constexpr int kSlots = S::kSlots;
     extern __shared__ __align__(16) unsigned char smem[];
-    int32_t *s_list = reinterpret_cast<int32_t *>(smem);
-    int32_t *s_n = s_list + kMaxWidth;
-    int2 *s_meta = reinterpret_cast<int2 *>(smem + S::kHead);              // [2][kSlots]
-    T *s_k = reinterpret_cast<T *>(smem + S::kHead + S::kMeta);            // [2][kSlots][kRow]
-    T *s_v = s_k + 2 * S::kTile;
+    T *s_k = reinterpret_cast<T *>(smem);                                  // [2][kSlots][kRow]
+    T *s_v = s_k + 2 * S::kTile;                                           // [2][kSlots][kRow]
+    int32_t *s_meta = reinterpret_cast<int32_t *>(s_v + 2 * S::kTile);     // [2][kSlots]
+    int32_t *s_n = s_meta + 2 * kSlots, *s_list = s_n + 4;                 // [width]
 
     const Unit u = unit_of(p, blockIdx.x);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,7 +79,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
 
     const T *k = static_cast<const T *>(p.a.k) + u.b * p.c.k_stride[0] + u.kv_head * p.c.k_stride[1];
     const T *v = static_cast<const T *>(p.a.v) + u.b * p.c.v_stride[0] + u.kv_head * p.c.v_stride[1];
-    if (n_tiles > 0) stage_tile<T, DH>(p, u, s_list, slots, 0, k, v, s_k, s_v, s_meta);
+    const uint32_t sk0 = smem_u32(s_k), sv0 = smem_u32(s_v);
+    if (n_tiles > 0) stage_tile<T, DH>(p, u, s_list, slots, 0, k, v, sk0, sv0, s_meta);
     cp_async_commit();
 
     // This lane's two rows.  The 16 rows of a warp belong to one head (chunks
@@ -105,6 +113,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
         if (ok0) doc0 = dq[0];
         if (ok1) doc1 = dq[8];
     }
+    // keys below these are in sight; none to a row without a document
+    const int end = p.c.nk_tokens, causal = p.c.causal;
+    const int limit0 = docs && doc0 < 0 ? 0 : min(end, causal ? max(pos0 + 1, u.prefix) : end);
+    const int limit1 = docs && doc1 < 0 ? 0 : min(end, causal ? max(pos1 + 1, u.prefix) : end);
     float slope = 0.f;
     int near0 = 0, near1 = 0;
     if (bias) {
@@ -123,24 +135,22 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
     float o[DH / 8][4];
 #pragma unroll
     for (int nd = 0; nd < DH / 8; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // l: this lane's part
     const int lm_row = lane & 7, lm_mat = lane >> 3;
-    const int per_tile = max(1, kSlots >> p.shift);   // list entries a tile spans
+    // ldmatrix lanes: row (lane & 7) of matrix (lane >> 3); keys' matrices are
+    // keys 16 np + {0, 0, 8, 8}, dims 16 kk + {0, 8, 0, 8}, the values' the other way round
+    const uint32_t k_lane = (uint32_t)((lm_row + ((lm_mat >> 1) << 3)) * S::kRow + ((lm_mat & 1) << 3)) * 2;
+    const uint32_t v_lane = (uint32_t)((lm_row + ((lm_mat & 1) << 3)) * S::kRow + ((lm_mat >> 1) << 3)) * 2;
 
     for (int e = 0; e < n_tiles; ++e) {
         const int st = e & 1;
         if (e + 1 < n_tiles)
-            stage_tile<T, DH>(p, u, s_list, slots, e + 1, k, v, s_k + (st ^ 1) * S::kTile, s_v + (st ^ 1) * S::kTile,
+            stage_tile<T, DH>(p, u, s_list, slots, e + 1, k, v, sk0 + (st ^ 1) * S::kTile * 2, sv0 + (st ^ 1) * S::kTile * 2,
                               s_meta + (st ^ 1) * kSlots);
         cp_async_commit();
         cp_async_wait_one();
         __syncthreads();
-        const T *sk = s_k + st * S::kTile;
-        const T *sv = s_v + st * S::kTile;
-        const int2 *meta = s_meta + st * kSlots;
-        const int first = (e * kSlots) >> p.shift;
-        bool full = (e + 1) * kSlots <= slots;
-        for (int i = 0; i < per_tile && full; ++i) full = (s_list[first + i] & kChunkFull) != 0;
+        const uint32_t sk = sk0 + st * S::kTile * 2 + k_lane, sv = sv0 + st * S::kTile * 2 + v_lane;
 
         float s[kSlots / 8][4];
 #pragma unroll
@@ -149,45 +159,58 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
         for (int kk = 0; kk < DH / 16; ++kk) {
 #pragma unroll
             for (int np = 0; np < kSlots / 16; ++np) {
-                const int key = np * 16 + lm_row + ((lm_mat >> 1) << 3);
-                const int dim = kk * 16 + ((lm_mat & 1) << 3);
                 uint32_t b0, b1, b2, b3;
-                ldmatrix_x4(smem_u32(sk + key * S::kRow + dim), b0, b1, b2, b3);
+                ldmatrix_x4(sk + (np * 16 * S::kRow + kk * 16) * 2, b0, b1, b2, b3);
                 Half<T>::mma(s[2 * np], qf[kk], b0, b1);
                 Half<T>::mma(s[2 * np + 1], qf[kk], b2, b3);
             }
         }
 
         // Scores in base 2.  Column of s[n][c]: 8n + 2t + (c & 1); row: c >> 1.
+        float mul = p.s1;
         if (cap) {
+            mul = 1.f;
 #pragma unroll
             for (int n = 0; n < kSlots / 8; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) s[n][c] = p.s2 * tanh_f32(s[n][c] * p.s1);
-        } else {
-#pragma unroll
-            for (int n = 0; n < kSlots / 8; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) s[n][c] *= p.s1;
         }
-        if (bias || !full) {
+        // 16 columns at a time: they are of one chunk
 #pragma unroll
-            for (int n = 0; n < kSlots / 8; ++n) {
+        for (int n2 = 0; n2 < kSlots / 8; n2 += 2) {
+            const int at = (e * kSlots + 8 * n2) >> p.shift;
+            const int entry = at < n_list ? s_list[at] : -1;
+            const bool full = entry >= 0 && (entry & kChunkFull);
+            if (!bias && full) continue;
+            const int base = entry < 0 ? 0 : ((entry & kChunkId) << p.shift) + ((8 * n2) & (p.c.chunk - 1)) + 2 * t;
+            if (bias) {
+                const float from0 = (float)(pos0 - base), from1 = from0 + 8.f, n0 = (float)near0, n1 = (float)near1;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int2 key = meta[n * 8 + 2 * t + (c & 1)];
-                    const int pos = c < 2 ? pos0 : pos1;
-                    float x = s[n][c];
-                    if (bias) x -= slope * (float)(abs(pos - key.x) - (c < 2 ? near0 : near1));
-                    if (!full) {
-                        bool see = key.x >= 0 && in_sight(p, u.prefix, pos, key.x);
-                        if (docs) see = see && key.y >= 0 && key.y == (c < 2 ? doc0 : doc1);
-                        if (!see) x = -INFINITY;
+                    const float col = (float)(8 * (c >> 1) + (c & 1));
+                    float *x = s[n2 + (c >> 1)];
+                    x[c & 1] = fmaf(-slope, fabsf(from0 - col) - n0, x[c & 1] * mul);
+                    x[2 + (c & 1)] = fmaf(-slope, fabsf(from1 - col) - n1, x[2 + (c & 1)] * mul);
+                }
+            }
+            if (!full) {
+                const int left0 = entry < 0 ? 0 : limit0 - base, left1 = entry < 0 ? 0 : limit1 - base;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int col = 8 * (c >> 1) + (c & 1);
+                    float *x = s[n2 + (c >> 1)];
+                    bool see0 = col < left0, see1 = col < left1;
+                    if (docs) {
+                        const int dk = s_meta[st * kSlots + 8 * n2 + 2 * t + col];
+                        see0 = see0 && dk == doc0;
+                        see1 = see1 && dk == doc1;
                     }
-                    s[n][c] = x;
+                    if (!see0) x[c & 1] = -INFINITY;
+                    if (!see1) x[2 + (c & 1)] = -INFINITY;
                 }
             }
         }
+        if (bias) mul = 1.f;
 
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -195,35 +218,44 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
             mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
             mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
         }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 2));
-        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-        const float base0 = mn0 == -INFINITY ? 0.f : mn0;
-        const float base1 = mn1 == -INFINITY ? 0.f : mn1;
-        const float corr0 = exp2f(m0 - base0), corr1 = exp2f(m1 - base1);
-        m0 = mn0;
-        m1 = mn1;
-        float ls0 = 0.f, ls1 = 0.f;
+        mx0 *= mul;
+        mx1 *= mul;
+        if (__any_sync(kFull, mx0 > m0 + kSlack || mx1 > m1 + kSlack)) {
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, d));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, d));
+            }
+            const float was0 = m0, was1 = m1;
+            m0 = fmaxf(m0, mx0);
+            m1 = fmaxf(m1, mx1);
+            // a row with no visible key so far keeps m = -inf
+            const float corr0 = was0 == -INFINITY ? 0.f : ex2(was0 - m0), corr1 = was1 == -INFINITY ? 0.f : ex2(was1 - m1);
+            l0 *= corr0;
+            l1 *= corr1;
+#pragma unroll
+            for (int nd = 0; nd < DH / 8; ++nd) {
+                o[nd][0] *= corr0;
+                o[nd][1] *= corr0;
+                o[nd][2] *= corr1;
+                o[nd][3] *= corr1;
+            }
+        }
+        const float ref0 = m0 == -INFINITY ? 0.f : kLift - m0, ref1 = m1 == -INFINITY ? 0.f : kLift - m1;
+        float la0 = 0.f, lb0 = 0.f, la1 = 0.f, lb1 = 0.f;
 #pragma unroll
         for (int n = 0; n < kSlots / 8; ++n) {
-            s[n][0] = exp2f(s[n][0] - base0);
-            s[n][1] = exp2f(s[n][1] - base0);
-            s[n][2] = exp2f(s[n][2] - base1);
-            s[n][3] = exp2f(s[n][3] - base1);
-            ls0 += s[n][0] + s[n][1];
-            ls1 += s[n][2] + s[n][3];
+            s[n][0] = ex2(fmaf(s[n][0], mul, ref0));
+            s[n][1] = ex2(fmaf(s[n][1], mul, ref0));
+            s[n][2] = ex2(fmaf(s[n][2], mul, ref1));
+            s[n][3] = ex2(fmaf(s[n][3], mul, ref1));
+            la0 += s[n][0];
+            lb0 += s[n][1];
+            la1 += s[n][2];
+            lb1 += s[n][3];
         }
-        l0 = l0 * corr0 + ls0;
-        l1 = l1 * corr1 + ls1;
-#pragma unroll
-        for (int nd = 0; nd < DH / 8; ++nd) {
-            o[nd][0] *= corr0;
-            o[nd][1] *= corr0;
-            o[nd][2] *= corr1;
-            o[nd][3] *= corr1;
-        }
+        l0 += la0 + lb0;
+        l1 += la1 + lb1;
 #pragma unroll
         for (int kk = 0; kk < kSlots / 16; ++kk) {
             const uint32_t pa[4] = {Half<T>::pack(s[2 * kk][0], s[2 * kk][1]), Half<T>::pack(s[2 * kk][2], s[2 * kk][3]),
@@ -231,10 +263,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
                                     Half<T>::pack(s[2 * kk + 1][2], s[2 * kk + 1][3])};
 #pragma unroll
             for (int dp = 0; dp < DH / 16; ++dp) {
-                const int key = kk * 16 + lm_row + ((lm_mat & 1) << 3);
-                const int dim = dp * 16 + ((lm_mat >> 1) << 3);
                 uint32_t b0, b1, b2, b3;
-                ldmatrix_x4_trans(smem_u32(sv + key * S::kRow + dim), b0, b1, b2, b3);
+                ldmatrix_x4_trans(sv + (kk * 16 * S::kRow + dp * 16) * 2, b0, b1, b2, b3);
                 Half<T>::mma(o[2 * dp], pa, b0, b1);
                 Half<T>::mma(o[2 * dp + 1], pa, b2, b3);
             }
@@ -265,8 +295,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) masked_attention_kernel(con
     if (p.a.lse && t == 0) {
         float *lse = p.a.lse + ((size_t)u.b * p.c.q_heads + head) * p.c.nq_tokens + token;
         const float unit = bias ? p.a.slopes[head] : 0.f;
-        if (ok0) lse[0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * kLn2 - unit * (float)near0;
-        if (ok1) lse[8] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * kLn2 - unit * (float)near1;
+        if (ok0) lse[0] = l0 == 0.f ? -INFINITY : (m0 - kLift + log2f(l0)) * kLn2 - unit * (float)near0;
+        if (ok1) lse[8] = l1 == 0.f ? -INFINITY : (m1 - kLift + log2f(l1)) * kLn2 - unit * (float)near1;
     }
     // rows to compute on their own, one bit for each of the warp's 16
     // (where the sum is a NaN, a score that the row sees is one, and so is the row)
@@ -283,11 +313,12 @@ template <typename T, int DH>
 cudaError_t launch(const Masked &p, unsigned units, cudaStream_t s) {
     using S = Shape<DH>;
     auto kern = masked_attention_kernel<T, DH>;
+    const int list = 16 + 4 * p.c.width;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem, done);
+    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem + 16 + 4 * kMaxWidth, done);
     if (e != cudaSuccess) return e;
     const int warps = min(kMaxWarps, (p.group << p.shift) / 16);
-    kern<<<units * (unsigned)p.tiles, 32 * warps, S::kSmem, s>>>(p);
+    kern<<<units * (unsigned)p.tiles, 32 * warps, S::kSmem + list, s>>>(p);
     return cudaGetLastError();
 }
 
