@@ -309,27 +309,40 @@ __global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_a
         queue[i][1] = queue[W::kPairs - 1][1];
     }
 
-    // queries
-    for (int r = warp; r < kRows; r += kAttnWarps) {
-        const int row = row0 + r;
-        float x[DH / 32];
+    // queries: eight lanes a row, DH / 8 elements each
+    for (int r = warp * 4 + lane / 8; r < kRows; r += kAttnWarps * 4) {
+        const int row = row0 + r, at8 = (lane & 7) * (DH / 8);
+        float x[DH / 8];
         unsigned amax = 0;
 #pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
-            x[i] = 0.f;
+        for (int i = 0; i < DH / 8; i += 8) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (row < p.rows) {
                 const int64_t at = b * p.n.q_stride[0] + (row / p.group) * p.n.q_stride[1] +
-                                   (head * p.group + row % p.group) * p.n.q_stride[2] + lane + 32 * i;
-                x[i] = p.n.dtype == RR_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.q)[at])
-                                            : __half2float(static_cast<const __half *>(p.a.q)[at]);
+                                   (head * p.group + row % p.group) * p.n.q_stride[2] + at8 + i;
+                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.a.q) + at));
             }
-            amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-        }
-        amax = __reduce_max_sync(kFull, amax);
-        const int shift = query_shift(amax);
+            const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < DH / 32; ++i) s_q[r * kQRow + lane + 32 * i] = __float2half_rn(ldexpf(x[i], shift));
-        if (lane == 0) s_row[r] = ldexpf(p.s1, -shift);
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = p.n.dtype == RR_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h[e]))
+                                                      : __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+                x[i + 2 * e] = f.x;
+                x[i + 2 * e + 1] = f.y;
+                amax = max(amax, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+            }
+        }
+        const unsigned group_mask = 0xffu << (lane & 24);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) amax = max(amax, __shfl_xor_sync(group_mask, amax, d));
+        const int shift = query_shift(amax);
+        // 2^shift in two factors: a shift can be as large as 162
+        const float half0 = __uint_as_float((unsigned)(127 + shift / 2) << 23);
+        const float half1 = __uint_as_float((unsigned)(127 + shift - shift / 2) << 23);
+#pragma unroll
+        for (int i = 0; i < DH / 8; i += 2)
+            *reinterpret_cast<uint32_t *>(s_q + r * kQRow + at8 + i) = pack_f16(x[i] * half0 * half1, x[i + 1] * half0 * half1);
+        if ((lane & 7) == 0) s_row[r] = ldexpf(p.s1, -shift);
     }
     // The distance that the bias is taken relative to: the newest token's to the
     // nearest key that has a page (see `nearest` of the masked attention).
