@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
     const Unit u = unit_of(p, blockIdx.x);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int n_list = build_list(p, u, s_list, s_n);
+    const int n_list = build_list(BlockTeam(), p, u, s_list, s_n);
     const int slots = n_list << p.shift;
     const int n_tiles = (slots + kSlots - 1) / kSlots;
 

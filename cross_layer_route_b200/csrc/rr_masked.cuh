@@ -74,17 +74,31 @@ __device__ __forceinline__ void lane_min_max(const int32_t *x, int n, int &lo, i
     }
 }
 
+// The threads that build a list together: all of a block, or two warps of it.
+struct BlockTeam {
+    __device__ __forceinline__ int rank() const { return threadIdx.x; }
+    __device__ __forceinline__ int size() const { return blockDim.x; }
+    __device__ __forceinline__ void sync() const { __syncthreads(); }
+};
+template <int FIRST, int THREADS, int BARRIER>
+struct PartTeam {
+    __device__ __forceinline__ int rank() const { return threadIdx.x - FIRST; }
+    __device__ __forceinline__ int size() const { return THREADS; }
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"n"(BARRIER), "n"(THREADS) : "memory"); }
+};
+
 // The unit's route in shared memory: list[0..n-1] = key chunks that can hold a
 // visible key, in route order, kChunkFull set where all of their keys are
 // visible to all rows (neither the masks nor the last chunk's end cut them).
-// By the whole block; ends with a barrier.
-__device__ __forceinline__ int build_list(const Masked &p, const Unit &u, int32_t *list, int32_t *n_out) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+// By a team; ends with its barrier.
+template <typename Team>
+__device__ __forceinline__ int build_list(const Team team, const Masked &p, const Unit &u, int32_t *list, int32_t *n_out) {
+    const int warp = team.rank() >> 5, lane = threadIdx.x & 31, warps = team.size() >> 5;
     const int32_t *route =
         p.a.route + (((size_t)u.b * p.c.route_heads + u.route_head) * p.nqc + u.i) * (size_t)p.c.route_stride;
     const int width = p.c.width;
     const bool causal = p.c.causal != 0, docs = p.a.doc_q != nullptr;
-    for (int e = threadIdx.x; e < width; e += blockDim.x) {
+    for (int e = team.rank(); e < width; e += team.size()) {
         int j = route[e];
         if (j < 0 || j >= p.nkc) j = -1;
         if (j >= 0) {
@@ -100,7 +114,7 @@ __device__ __forceinline__ int build_list(const Masked &p, const Unit &u, int32_
     }
     int qlo = 0, qhi = 0;
     if (docs) lane_min_max(p.a.doc_q + (size_t)u.b * p.c.nq_tokens + (u.i << p.shift), u.tokens, qlo, qhi);
-    __syncthreads();
+    team.sync();
     if (docs) {
         // documents are mostly runs of tokens: a chunk of one document is either
         // visible to a query chunk of one document as a whole or not at all
@@ -126,7 +140,7 @@ __device__ __forceinline__ int build_list(const Masked &p, const Unit &u, int32_
                 }
             }
         }
-        __syncthreads();
+        team.sync();
     }
     if (warp == 0) {
         int n = 0;
@@ -140,7 +154,7 @@ __device__ __forceinline__ int build_list(const Masked &p, const Unit &u, int32_
         }
         if (lane == 0) *n_out = n;
     }
-    __syncthreads();
+    team.sync();
     return *n_out;
 }
 
