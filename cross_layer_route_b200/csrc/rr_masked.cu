@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
                     const int col = 8 * (c >> 1) + (c & 1);
                     float *x = s[n2 + (c >> 1)];
                     bool see0 = col < left0, see1 = col < left1;
-                    if (docs) {
+                    if (entry >= 0 && (entry & kChunkCut)) {
                         const int dk = s_meta[st * kSlots + 8 * n2 + 2 * t + col];
                         see0 = see0 && dk == doc0;
                         see1 = see1 && dk == doc1;

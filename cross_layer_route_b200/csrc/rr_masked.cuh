@@ -22,7 +22,8 @@ using rr_attn::kMaxWidth;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kChunkFull = 1 << 30;   // list flag: every key of the chunk is visible to every row
-constexpr int kChunkId = kChunkFull - 1;
+constexpr int kChunkCut = 1 << 29;    // ... its documents differ from row to row or key to key
+constexpr int kChunkId = kChunkCut - 1;
 
 struct Masked {
     rr_masked_attn_config c;
@@ -89,7 +90,8 @@ struct PartTeam {
 
 // The unit's route in shared memory: list[0..n-1] = key chunks that can hold a
 // visible key, in route order, kChunkFull set where all of their keys are
-// visible to all rows (neither the masks nor the last chunk's end cut them).
+// visible to all rows (neither the masks nor the last chunk's end cut them),
+// kChunkCut where the documents cut them.
 // By a team; ends with its barrier.
 template <typename Team>
 __device__ __forceinline__ int build_list(const Team team, const Masked &p, const Unit &u, int32_t *list, int32_t *n_out) {
@@ -136,7 +138,7 @@ __device__ __forceinline__ int build_list(const Team team, const Masked &p, cons
                 khi[i] = __reduce_max_sync(kFull, khi[i]);
                 if (lane == 0 && j[i] >= 0) {
                     if (khi[i] < 0 || qhi < 0 || khi[i] < qlo || klo[i] > qhi) list[e0 + i] = -1;
-                    else if (klo[i] != khi[i] || qlo != qhi) list[e0 + i] = j[i] & ~kChunkFull;
+                    else if (klo[i] != khi[i] || qlo != qhi) list[e0 + i] = (j[i] & ~kChunkFull) | kChunkCut;
                 }
             }
         }
@@ -177,7 +179,7 @@ __device__ __forceinline__ int nearest(const Masked &p, const Unit &u, const int
         if (hi <= lo) continue;
         const int d = pos < lo ? lo - pos : pos >= hi ? pos - (hi - 1) : 0;
         if (d >= best) continue;
-        if (!p.a.doc_q || (list[e] & kChunkFull)) {
+        if (!(list[e] & kChunkCut)) {
             best = d;
         } else {
             const int32_t *dk = p.a.doc_k + (size_t)u.b * p.c.nk_tokens;

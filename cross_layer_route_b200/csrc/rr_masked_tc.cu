@@ -299,7 +299,8 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     const int mine = j * per + lane < n_list ? list[j * per + lane] : -1;
                     const bool plain = __all_sync(kFull, lane >= per || (mine >= 0 && (mine & kChunkFull)));
                     int dk[4];
-                    if (docs && !plain) {
+                    const bool cut = __any_sync(kFull, lane < per && mine >= 0 && (mine & kChunkCut));
+                    if (cut) {
                         const int entry = __shfl_sync(kFull, mine, (4 * lane) >> p.shift);
                         const int at = ((entry & kChunkId) << p.shift) + ((4 * lane) & (p.c.chunk - 1));
 #pragma unroll
@@ -351,7 +352,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
 #pragma unroll
                             for (int c = 0; c < 16; ++c) s[c0 + c] = c < left ? s[c0 + c] : -INFINITY;
                         }
-                        if (docs) {
+                        if (cut) {
 #pragma unroll
                             for (int c = 0; c < kTileKeys; ++c)
                                 if (__shfl_sync(kFull, dk[c & 3], c >> 2) != doc) s[c] = -INFINITY;
