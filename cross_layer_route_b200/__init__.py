@@ -405,12 +405,18 @@ def _on_stream(index: int, stream, call, *args):
 
 
 def _int32(name, t, shape, index):
-    """Address of a contiguous int32 tensor of this shape (None: any size there)."""
-    got = t.shape
-    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous() or len(got) != len(shape) \
-            or (got != shape and any(n is not None and n != m for n, m in zip(shape, got))):
+    """Address of a contiguous int32 tensor of this shape."""
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous int32 {shape} on cuda:{index}, got {_describe(t)}")
     return t.data_ptr()
+
+
+def _dim(name, t, dims, i):
+    """Size i of a tensor that should have `dims` dimensions."""
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: expected {dims} dimensions, got {_describe(t)}")
+    return shape[i]
 
 
 def _slopes(t, heads, index):
@@ -425,12 +431,14 @@ def _rows_like(name, t, dtype, shape, index):
     """Strides, all but the last, of a tensor of this type and shape whose rows
     are contiguous; that of a size of one counts nothing."""
     st = t.stride()
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or st[-1] != 1:
+    if t.dtype is not dtype or t.shape != shape or st[-1] != 1 or t.get_device() != index:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{index}, the last dimension contiguous, "
                          f"got {_describe(t)}")
-    if 1 in shape:
-        return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], st))
-    return st[:-1]
+    return _strides(st, shape) if 1 in shape else st[:-1]
+
+
+def _strides(strides, shape):
+    return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], strides))
 
 
 def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: torch.Tensor, chunk: int,
@@ -459,8 +467,8 @@ def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: t
     kv_shape = (batch, kv_heads, nk, dh)
     strides = _rows_like("q", q, dtype, shape, index) + _rows_like("k", k, dtype, kv_shape, index) \
         + _rows_like("v", v, dtype, kv_shape, index)
-    d_route = _int32("route", route, (batch, None, -(-nq // chunk) if chunk > 0 else 0, None), index)
-    route_heads, stride = route.shape[1], route.shape[3]
+    route_heads, stride = _dim("route", route, 4, 1), route.shape[3]
+    d_route = _int32("route", route, (batch, route_heads, -(-nq // chunk) if chunk > 0 else 0, stride), index)
     width = stride if width is None else int(width)
     if width > stride:
         raise ValueError(f"width {width} is larger than the route's {stride} entries")
@@ -472,17 +480,21 @@ def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: t
             0 if doc_q is None else _int32("doc_q", doc_q, (batch, nq), index),
             0 if doc_k is None else _int32("doc_k", doc_k, (batch, nk), index),
             0 if prefix is None else _int32("prefix", prefix, (batch,), index))
+    if out is not None:
+        _rows_like("out", out, dtype, shape, index)
     return _on_stream(index, stream, _masked_attention, q, out, return_lse, ints, ptrs)
 
 
 def _masked_attention(handle, q, out, return_lse, ints, ptrs):
+    shape = q.shape
     if out is None:
         out = torch.empty_like(q)
-    out_strides = _rows_like("out", out, q.dtype, q.shape, q.get_device())
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
-    _check(_lib.rr_masked_attention(_MASKED_CFG.pack(*ints, *out_strides),
-                                    _MASKED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),
-                                    handle), "rr_masked_attention")
+    lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    status = _lib.rr_masked_attention(_MASKED_CFG.pack(*ints, *_strides(out.stride(), shape)),
+                                      _MASKED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),
+                                      handle)
+    if status:
+        raise RRError(status, "rr_masked_attention")
     return (out, lse) if return_lse else out
 
 
@@ -520,8 +532,8 @@ def cache_empty(pages: int, heads: int, chunk: int, dh: int, fmt: str = "e4m3", 
 
 
 def _ragged(rows, cu, start, table, index):
-    d_table = _int32("table", table, (None, None), index)
-    batch, width = table.shape
+    batch, width = _dim("table", table, 2, 0), table.shape[1]
+    d_table = _int32("table", table, (batch, width), index)
     return _CACHE_ROWS.pack(batch, rows, _int32("cu", cu, (batch + 1,), index),
                             _int32("start", start, (batch,), index), d_table, width, max(width, 1))
 
@@ -595,12 +607,12 @@ def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
     batch, q_tokens, q_heads, dh = shape
     cfg, pool, index, heads = _cache(codes, scales, dh)
     q_strides = _rows_like("q", q, dtype, shape, index)
-    d_table = _int32("table", table, (batch, None), index)
-    table_width = table.shape[1]
+    table_width = _dim("table", table, 2, 1)
+    d_table = _int32("table", table, (batch, table_width), index)
     stride, d_route = 1, 0
     if route is not None:
-        d_route = _int32("route", route, (batch, heads, None), index)
-        stride = route.shape[2]
+        stride = _dim("route", route, 3, 2)
+        d_route = _int32("route", route, (batch, heads, stride), index)
         width = stride if width is None else int(width)
         if width > stride:
             raise ValueError(f"width {width} is larger than the route's {stride} entries")
