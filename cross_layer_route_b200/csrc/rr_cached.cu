@@ -24,6 +24,7 @@
 // The references move only when a score passes them by 2^8: most steps then
 // cost one vote and no shuffles.
 // A warp copies its steps (cp.async) into a ring of its own, two or three ahead.
+#include <cooperative_groups.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -40,6 +41,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAttnWarps = 6;
 constexpr int kJoinWarps = 4;
+constexpr int kMaxCluster = 8;   // blocks of a cluster
 constexpr float kLift = 7.f;     // weights are 2^7 at the maximum
 constexpr float kSlack = 8.f;    // ... and 2^15 at most
 constexpr int kGroupLift = 12;   // codes of 4 bits carry 2^12
@@ -53,10 +55,11 @@ struct Cached {
     rr_cache_pool pool;
     rr_cached_attn_config n;
     rr_cached_attn_args a;
-    float *part;       // [batch * heads, splits, rows, dh + kState]
+    float *part;       // [batch * heads, splits, rows, dh + kState], without a cluster
     int shift;         // log2(chunk)
     int group, rows;   // query heads per key head, rows per key head
     int splits;
+    bool cluster;      // the splits are a cluster of blocks
     float s1, s2;      // as in the masked attention
 };
 
@@ -236,6 +239,30 @@ __device__ __forceinline__ int query_shift(unsigned amax_bits) {
     return e == 0 || e == 255 ? 0 : 13 - (e - 127);
 }
 
+// Two dims of one row's result from its sums: o relative to 2^(n2 - kLift) of the
+// weights', their sum to 2^n1; dim 0's caller writes lse.
+template <int DH>
+__device__ __forceinline__ void write_out(const Cached &p, int b, int head, int row, int dim, float x, float y, float n1,
+                                          float sum, float n2, float near) {
+    const bool none = sum == 0.f;
+    const float f = none ? 0.f : ex2(n2 - kLift) / sum;
+    x = none ? 0.f : x * f;
+    y = none ? 0.f : y * f;
+    const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
+    static_cast<uint32_t *>(p.a.out)[(orow * DH + dim) / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
+    if (p.a.lse && dim == 0)
+        p.a.lse[orow] = none ? -INFINITY
+                             : (n1 + log2f(sum)) * kLn2 -
+                                   (p.a.slopes ? p.a.slopes[head * p.group + row % p.group] * near : 0.f);
+}
+
+// The ring's memory, which also takes the warps' states when they are joined.
+template <int FMT, int DH, int NT>
+__host__ __device__ constexpr int joined_bytes() {
+    const int ring = kAttnWarps * Words<FMT, DH>::kRing, states = kAttnWarps * 32 * (DH / 16 * 4 * NT + 6 * NT) * 4;
+    return ring > states ? ring : states;
+}
+
 template <int FMT, int DH, int NT>
 __global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_attention_kernel(const __grid_constant__ Cached p) {
     using W = Words<FMT, DH>;
@@ -249,6 +276,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_a
     int *s_near = reinterpret_cast<int *>(s_row + kRows);
     unsigned char *s_ring = smem + kRows * kQRow * 2 + kRows * 4 + kGap;    // [warps][stages][stage]
     float *s_merge = reinterpret_cast<float *>(s_ring);                               // after the loop
+    float *s_part = reinterpret_cast<float *>(s_ring + joined_bytes<FMT, DH, NT>());  // [kRows][DH + kState]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y % p.c.heads, b = blockIdx.y / p.c.heads, row0 = blockIdx.z * kRows;
@@ -737,23 +765,60 @@ __global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_a
             const int dim = (DH / 8) * g + 2 * i;
             const int back = p.n.q_tokens - 1 - row / p.group, near = max(0, *s_near - back);
             if (p.splits > 1) {
-                float *part = p.part + (((size_t)blockIdx.y * p.splits + blockIdx.x) * p.rows + row) * (DH + kState);
+                float *part = p.cluster
+                                  ? s_part + (row - row0) * (DH + kState)
+                                  : p.part + (((size_t)blockIdx.y * p.splits + blockIdx.x) * p.rows + row) * (DH + kState);
                 *reinterpret_cast<float2 *>(part + dim) = make_float2(x, y);
                 if (g == 0 && i == 0) *reinterpret_cast<float4 *>(part + DH) = make_float4(n1, sum, n2, (float)near);
             } else {
-                const bool none = sum == 0.f;
-                const float f = none ? 0.f : ex2(n2 - kLift) / sum;
-                x = none ? 0.f : x * f;
-                y = none ? 0.f : y * f;
-                const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
-                static_cast<uint32_t *>(p.a.out)[(orow * DH + dim) / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
-                if (p.a.lse && g == 0 && i == 0)
-                    p.a.lse[orow] = none ? -INFINITY
-                                         : (n1 + log2f(sum)) * kLn2 -
-                                               (bias ? p.a.slopes[head * p.group + row % p.group] * (float)near : 0.f);
+                write_out<DH>(p, b, head, row, dim, x, y, n1, sum, n2, (float)near);
             }
         }
     }
+    if (!p.cluster) return;
+    // The blocks that share these tokens are a cluster: each joins a part of the
+    // results out of all blocks' shared memory.
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    const int valid = min(kRows, p.rows - row0);
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < valid * (DH / 2); i += p.splits * blockDim.x) {
+        const int r = i / (DH / 2), dim = i % (DH / 2) * 2;
+        float n1 = -INFINITY, n2 = -INFINITY, near = 0.f;
+        float4 st[kMaxCluster];
+        float2 xy[kMaxCluster];
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+            if (s < p.splits) {
+                const float *at = cluster.map_shared_rank(s_part, s) + r * (DH + kState);
+                st[s] = *reinterpret_cast<const float4 *>(at + DH);
+                xy[s] = *reinterpret_cast<const float2 *>(at + dim);
+                n1 = fmaxf(n1, st[s].x);
+                near = st[s].w;
+            }
+        }
+        const float b1 = n1 == -INFINITY ? 0.f : n1;
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+            if (s < p.splits) {
+                st[s].x -= b1;
+                st[s].z += st[s].x;
+                n2 = fmaxf(n2, st[s].z);
+            }
+        }
+        const float b2 = n2 == -INFINITY ? 0.f : n2;
+        float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+            if (s < p.splits) {
+                const float f = ex2(st[s].z - b2);
+                sum += st[s].y * ex2(st[s].x);
+                x += xy[s].x * f;
+                y += xy[s].y * f;
+            }
+        }
+        write_out<DH>(p, b, head, row0 + r, dim, x, y, n1, sum, n2, near);
+    }
+    cluster.sync();      // no block leaves while its memory is read
 }
 
 // Joins the splits of one row: a block per row, its warps take splits in turn,
@@ -765,7 +830,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __gr
     __shared__ float s_o[kJoinWarps][DH], s_l[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.x / p.rows, row = blockIdx.x % p.rows, head = bh % p.c.heads, b = bh / p.c.heads;
-    const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
     const float *at = p.part + ((size_t)bh * p.splits * p.rows + row) * (DH + kState);
     const size_t stride = (size_t)p.rows * (DH + kState);
 #if __CUDA_ARCH__ >= 900
@@ -809,15 +873,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __gr
         x += s_o[w][d];
         y += s_o[w][d + 1];
     }
-    const bool none = l == 0.f;
-    const float f = none ? 0.f : ex2(n2 - kLift) / l;
-    x = none ? 0.f : x * f;
-    y = none ? 0.f : y * f;
-    static_cast<uint32_t *>(p.a.out)[(orow * DH + d) / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
-    if (p.a.lse && threadIdx.x == 0)
-        p.a.lse[orow] = none ? -INFINITY
-                             : (n1 + log2f(l)) * kLn2 -
-                                   (p.a.slopes ? p.a.slopes[head * p.group + row % p.group] * at[DH + 3] : 0.f);
+    write_out<DH>(p, b, head, row, d, x, y, n1, l, n2, at[DH + 3]);
 }
 
 bool config_ok(const rr_cache_config *c, const rr_cached_attn_config *n) {
@@ -841,41 +897,62 @@ int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
-// CTAs that share a sequence's tokens.  A CTA costs its share of the steps and
-// a start and an end worth about 24 of them; CTAs come in waves of 148 SMs, of
-// which the last is half empty when there is more than one.  Measured: 16
-// sequences of 512 steps and 8 heads, 2 CTAs each (256 in one wave) 72 us, 3
-// (two waves) 88 us; 64 sequences of up to 751 steps, 1 CTA each 250 us, 2
-// 216 us, 3 223 us.  No CTA gets less than a pair of steps for each warp.
-int splits_of(const rr_cache_config *c, const rr_cached_attn_config *n, bool route) {
+// CTAs that share a sequence's tokens, and how their results are joined.  A CTA
+// costs its share of the steps and a start and an end worth about 24 of them;
+// CTAs come in waves of 148 SMs, of which the last is half empty when there is
+// more than one.  Measured: 16 sequences of 512 steps and 8 heads, 2 CTAs each
+// (256 in one wave) 72 us, 3 (two waves) 88 us; 64 sequences of up to 751 steps,
+// 1 CTA each 250 us, 2 216 us, 3 223 us.  No CTA gets less than a pair of steps
+// for each warp.  Joining through the workspace takes a second launch, for
+// caller and GPU together about 36 steps; a cluster needs none, but clusters do
+// not pack (24 sequences of 188 steps and 2 heads, 3 CTAs each in clusters 43 us,
+// joined through the workspace 26 us), so they are for at most half the SMs (one
+// sequence of 256 steps and 8 heads: 11.3 us and 18.7 with the caller's share, 12.7
+// and 28 through the workspace).
+struct Splits {
+    int n;
+    bool cluster;
+};
+Splits splits_of(const rr_cache_config *c, const rr_cached_attn_config *n, bool route) {
     const long long rows = (long long)(n->q_heads / c->heads) * n->q_tokens;
     const int nt = tiles_of(c, n), slots = 148 * ctas_per_sm(c->dh, nt);
     const long long blocks = (long long)n->batch * c->heads * ((rows + 8 * nt - 1) / (8 * nt));
     const long long steps = (long long)(route ? n->width : n->table_width) * (c->chunk / 16);
-    if (blocks == 0) return 1;
+    if (blocks == 0) return {1, false};
     const long long most = steps / (2 * kAttnWarps), tried = 4 * slots / blocks + 1;
-    int best = 1;
+    Splits best = {1, false};
     double least = 1e300;
     for (int s = 1; s == 1 || (s <= most && s <= tried); ++s) {
+        const bool cluster = s > 1 && s <= kMaxCluster && blocks * s <= 74;
         const double ctas = (double)blocks * s, waves = ctas <= slots ? 1.0 : ctas / slots + 0.5;
-        const double cost = waves * ((double)steps / s + 24.0);
-        if (cost < least) least = cost, best = s;
+        const double cost = waves * ((double)steps / s + 24.0) + (s > 1 && !cluster ? 36.0 : 0.0);
+        if (cost < least) least = cost, best = {s, cluster};
     }
     return best;
 }
 
 template <int FMT, int DH, int NT>
 cudaError_t launch(const Cached &p, cudaStream_t s) {
-    constexpr int kKeep = DH / 16 * 4 * NT + 6 * NT;
-    using W = Words<FMT, DH>;
-    const int ring = kAttnWarps * W::kRing, merge = kAttnWarps * 32 * kKeep * 4;
-    const int smem = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 +
-                     (ring > merge ? ring : merge);
+    const int smem = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 + joined_bytes<FMT, DH, NT>() + 8 * NT * (DH + kState) * 4;
     auto kern = cached_attention_kernel<FMT, DH, NT>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), smem, done);
     if (e != cudaSuccess) return e;
     const dim3 grid(p.splits, p.n.batch * p.c.heads, (p.rows + 8 * NT - 1) / (8 * NT));
+    if (p.cluster) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = p.splits;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t config = {};
+        config.gridDim = grid;
+        config.blockDim = dim3(32 * kAttnWarps);
+        config.dynamicSmemBytes = smem;
+        config.stream = s;
+        config.attrs = &attr;
+        config.numAttrs = 1;
+        return cudaLaunchKernelEx(&config, kern, p);
+    }
     kern<<<grid, 32 * kAttnWarps, smem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
@@ -906,9 +983,9 @@ extern "C" size_t rr_cached_attention_workspace_bytes(const rr_cache_config *cfg
                                                       int32_t routed) {
     using namespace rr_cache;
     if (!config_ok(cfg, attn)) return 0;
-    const int splits = splits_of(cfg, attn, routed != 0);
-    if (splits == 1) return 0;
-    return (size_t)attn->batch * attn->q_heads * attn->q_tokens * splits * (cfg->dh + kState) * sizeof(float);
+    const Splits splits = splits_of(cfg, attn, routed != 0);
+    if (splits.n == 1 || splits.cluster) return 0;
+    return (size_t)attn->batch * attn->q_heads * attn->q_tokens * splits.n * (cfg->dh + kState) * sizeof(float);
 }
 
 extern "C" rr_status rr_cached_attention(const rr_cache_config *cfg, const rr_cache_pool *pool,
@@ -936,7 +1013,9 @@ extern "C" rr_status rr_cached_attention(const rr_cache_config *cfg, const rr_ca
     p.shift = chunk_shift(cfg->chunk);
     p.group = attn->q_heads / cfg->heads;
     p.rows = p.group * attn->q_tokens;
-    p.splits = splits_of(cfg, attn, a.route != nullptr);
+    const Splits splits = splits_of(cfg, attn, a.route != nullptr);
+    p.splits = splits.n;
+    p.cluster = splits.cluster;
     const float scale = attn->scale > 0.f ? attn->scale : 1.0f / sqrtf((float)cfg->dh);
     p.s1 = attn->soft_cap > 0.f ? scale / attn->soft_cap : scale * kLog2e;
     p.s2 = attn->soft_cap * kLog2e;

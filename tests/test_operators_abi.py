@@ -146,11 +146,13 @@ def test_cached_attention_refuses_bad_pointers_and_workspaces():
     for bad in (dict(q=0), dict(q=P + 8), dict(out=0), dict(out=P + 2), dict(seq_lens=0), dict(seq_lens=P + 1),
                 dict(page_table=0), dict(page_table=P + 2), dict(route=P + 2), dict(slopes=P + 1), dict(lse=P + 2)):
         refused(rr.rr_cached_attention, cache(), pool, attn(), attn_args(**bad), P, 1 << 40, 0)
-    need = rr.rr_cached_attention_workspace_bytes(cache(), attn(), False)
-    assert need > 0 and need % (2 * 8 * (64 + 4) * 4) == 0
-    refused(rr.rr_cached_attention, cache(), pool, attn(), attn_args(), P, need - 1, 0, status=rr.RR_ENOMEM)
-    refused(rr.rr_cached_attention, cache(), pool, attn(), attn_args(), P + 16, need, 0)
-    refused(rr.rr_cached_attention, cache(), pool, attn(), attn_args(), 0, need, 0)
+    assert rr.rr_cached_attention_workspace_bytes(cache(), attn(), False) == 0     # a few blocks share a sequence
+    long = attn(batch=1, table_width=4096, table_stride=4096)
+    need = rr.rr_cached_attention_workspace_bytes(cache(), long, False)
+    assert need > 0 and need % (8 * (64 + 4) * 4) == 0
+    refused(rr.rr_cached_attention, cache(), pool, long, attn_args(), P, need - 1, 0, status=rr.RR_ENOMEM)
+    refused(rr.rr_cached_attention, cache(), pool, long, attn_args(), P + 16, need, 0)
+    refused(rr.rr_cached_attention, cache(), pool, long, attn_args(), 0, need, 0)
     refused(rr.rr_cached_attention, cache(), rr.rr_cache_pool(0, P), attn(), attn_args(), P, need, 0)
     rr.rr_cached_attention(cache(), pool, attn(batch=0), attn_args(), 0, 0, 0)
     rr.rr_cached_attention(cache(), pool, attn(q_tokens=0), attn_args(), 0, 0, 0)

@@ -364,7 +364,7 @@ def test_bias_of_far_positions_keeps_the_scores(rr):
 
 
 def test_streams_graphs_and_workspaces(rr):
-    codes, scales, fmt, q, lens, table = cached_case(lens=[1000, 300], group=4, dh=128)
+    codes, scales, fmt, q, lens, table = cached_case(lens=[20000, 300], group=4, heads=1, dh=128, chunk=64)
     args = (_i32(lens), _i32(table))
     want = rr.cached_attention(codes, scales, q, *args)
     side = torch.cuda.Stream()
@@ -373,7 +373,7 @@ def test_streams_graphs_and_workspaces(rr):
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got)
     cfg = rr.rr_cache_config(codes.shape[0], codes.shape[1], 128, codes.shape[3], rr.RR_E4M3)
-    n = rr.rr_cached_attn_config(2, 1, 8, rr.RR_BF16, table.shape[1], table.shape[1], 0, 1)
+    n = rr.rr_cached_attn_config(2, 1, 4, rr.RR_BF16, table.shape[1], table.shape[1], 0, 1)
     work = torch.empty(rr.rr_cached_attention_workspace_bytes(cfg, n, False), dtype=torch.uint8, device=DEV)
     assert work.numel() > 0
     assert torch.equal(rr.cached_attention(codes, scales, q, *args, workspace=work), want)
@@ -386,13 +386,13 @@ def test_streams_graphs_and_workspaces(rr):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             graphs.append((graph, rr.cached_attention(codes, scales, q, *args, workspace=work, return_lse=True)))
-    args[0].copy_(_i32([777, 1]))
+    args[0].copy_(_i32([17001, 1]))
     q.copy_(torch.randn_like(q))
     for graph, _ in graphs:
         graph.replay()
     torch.cuda.synchronize()
     for _, got in graphs:
-        check(got, codes, scales, fmt, q, [777, 1], table)
+        check(got, codes, scales, fmt, q, [17001, 1], table)
 
 
 def test_a_turn_written_read_and_attended(rr):
