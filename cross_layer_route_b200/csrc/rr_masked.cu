@@ -4,10 +4,11 @@
 //
 // One CTA = up to 64 rows of a unit (rr_masked.cuh), 16 rows per warp, so the
 // query heads that share a key head read its chunks once.  Keys are visited in
-// tiles of slots of the concatenated route (a tile holds several chunks, or a
-// part of one), staged by cp.async two tiles deep into rows padded by 16 bytes;
-// slots past the route are filled with zeros and masked.  S = q K^T and O += P V
-// on mma.sync with fp32 sums, P straight from the scores' registers, and
+// tiles of 64 slots of the concatenated route (a tile holds several chunks, or a
+// part of one), two tiles deep: by TMA into swizzled rows, a copy for each chunk
+// and 64 elements, or by cp.async into rows padded by 16 bytes (kTmaSlots says
+// when); slots past the route are filled with zeros and masked.  S = q K^T and
+// O += P V on mma.sync with fp32 sums, P straight from the scores' registers, and
 //   x = s2 tanh(s1 s) or s1 s           (base-2 scores)
 //   x -= slope (|pos - key| - near)      near: the row's nearest visible key
 //   x = -inf where the masks say so, looked at per element only in chunks that
@@ -21,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include "rr_masked.cuh"
+#include "rr_tc.cuh"
 
 namespace rr_masked {
 
@@ -30,22 +32,56 @@ constexpr int kMaxWarps = 4;    // 16 rows each
 constexpr float kSlack = 8.f;   // growth of the maximum that is let pass
 constexpr float kLift = 7.f;    // weights are 2^7 at the maximum
 
-template <int DH>
+// Slots that a call's units visit, at least, for the copies to go by TMA: it saves
+// the copies' instructions (8 heads of 4 prompts of 2501 tokens at dh 64, chunks
+// of 32, 1.9 M slots: 87 us, by cp.async 105 us), but its two tensor maps take the
+// caller 2 us, which shows in calls whose 20 us are the caller's anyway.
+constexpr long long kTmaSlots = 1 << 19;
+
+template <int DH, bool TMA>
 struct Shape {
     static constexpr int kSlots = 64;                           // key slots per tile
-    static constexpr int kRow = DH + 8;
-    static constexpr int kTile = kSlots * kRow;
+    static constexpr int kRow = TMA ? 64 : DH + 8;              // elements from a slot to the next
+    static constexpr int kSub = kSlots * 64;                    // TMA: elements of a tile's 64-element part
+    static constexpr int kTile = TMA ? kSlots * DH : kSlots * kRow;
     static constexpr int kMeta = 2 * kSlots * 4;                // documents per slot, two stages
-    static constexpr int kSmem = kMeta + 4 * kTile * 2;         // and the list
-    static constexpr int kMinBlocks = 3;                         // CTAs per SM: at most 168 registers, no spills in the loop
+    static constexpr int kAlign = TMA ? 1024 : 0;
+    static constexpr int kSmem = kAlign + 4 * kTile * 2 + kMeta + 32;     // and the list
+    static constexpr int kMinBlocks = 3;                        // CTAs per SM: at most 168 registers
 };
 
-// One tile of keys and values.  A thread copies the same 16-byte column of every
+// The two ways' tensor maps, or nothing.
+struct TileMaps {
+    CUtensorMap k, v;
+    int axes[2];
+};
+
+// One tile of keys and values by TMA, by one warp: a lane for each copy.
+template <int DH>
+__device__ __forceinline__ void stage_tile_tma(const Masked &p, const Unit &u, const TileMaps &maps, const int32_t *list,
+                                               int slots, int tile, uint32_t sk, uint32_t sv, uint64_t *bar) {
+    using S = Shape<DH, true>;
+    const int lane = threadIdx.x & 31, box = min(p.c.chunk, S::kSlots), per = S::kSlots / box;
+    if (lane == 0) rr::tc::mbar_expect_tx(bar, 2 * S::kTile * 2);
+    __syncwarp();
+    if (lane < 2 * per * (DH / 64)) {
+        const int side = lane & 1, sub = (lane >> 1) % (DH / 64), part = (lane >> 1) / (DH / 64);
+        const int slot = tile * S::kSlots + part * box;
+        // past the route: a box past the tokens, which reads as zeros
+        const int token = slot < slots ? ((list[slot >> p.shift] & kChunkId) << p.shift) + (slot & (p.c.chunk - 1))
+                                       : p.c.nk_tokens;
+        const int axes = maps.axes[side];
+        rr::tc::tma_load_4d((side ? sv : sk) + (sub * S::kSub + part * box * 64) * 2, side ? &maps.v : &maps.k, bar, sub * 64,
+                            token, axes & 1 ? u.kv_head : 0, axes & 2 ? u.b : 0);
+    }
+}
+
+// One tile of keys and values by cp.async.  A thread copies the same 16-byte column of every
 // (blockDim / (DH / 8))-th slot.
 template <typename T, int DH>
 __device__ __forceinline__ void stage_tile(const Masked &p, const Unit &u, const int32_t *list, int slots, int tile,
-                                           const T *k, const T *v, uint32_t sk, uint32_t sv, int32_t *meta) {
-    using S = Shape<DH>;
+                                           const T *k, const T *v, uint32_t sk, uint32_t sv) {
+    using S = Shape<DH, false>;
     const int c = (threadIdx.x % (DH / 8)) * 8, step = blockDim.x / (DH / 8);
     for (int r = threadIdx.x / (DH / 8); r < S::kSlots; r += step) {
         const int slot = tile * S::kSlots + r;
@@ -56,19 +92,38 @@ __device__ __forceinline__ void stage_tile(const Masked &p, const Unit &u, const
         const uint32_t to = (uint32_t)(r * S::kRow + c) * 2;
         cp_async16_zfill(sk + to, k + at * p.c.k_stride[2] + c, bytes);
         cp_async16_zfill(sv + to, v + at * p.c.v_stride[2] + c, bytes);
-        if (p.a.doc_k && c == 0) meta[r] = s >= 0 ? p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] : -1;
     }
 }
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_attention_kernel(const __grid_constant__ Masked p) {
-    using S = Shape<DH>;
+// The documents of a tile's slots.
+__device__ __forceinline__ void stage_documents(const Masked &p, const Unit &u, const int32_t *list, int slots, int tile,
+                                                int32_t *meta) {
+    for (int r = threadIdx.x; r < 64; r += blockDim.x) {
+        const int slot = tile * 64 + r;
+        const int s = slot < slots ? ((list[slot >> p.shift] & kChunkId) << p.shift) + (slot & (p.c.chunk - 1)) : INT_MAX;
+        meta[r] = s < p.c.nk_tokens ? p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] : -1;
+    }
+}
+
+template <typename T, int DH, bool TMA>
+__global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH, TMA>::kMinBlocks)
+masked_attention_kernel(const __grid_constant__ Masked p, const __grid_constant__ TileMaps maps) {
+    using S = Shape<DH, TMA>;
     constexpr int kSlots = S::kSlots;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(16) unsigned char raw[];
+    unsigned char *smem = TMA ? rr::tc::align_smem_1024(raw) : raw;
     T *s_k = reinterpret_cast<T *>(smem);                                  // [2][kSlots][kRow]
     T *s_v = s_k + 2 * S::kTile;                                           // [2][kSlots][kRow]
     int32_t *s_meta = reinterpret_cast<int32_t *>(s_v + 2 * S::kTile);     // [2][kSlots]
-    int32_t *s_n = s_meta + 2 * kSlots, *s_list = s_n + 4;                 // [width]
+    uint64_t *full = reinterpret_cast<uint64_t *>(s_meta + 2 * kSlots);    // [2]
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(full + 2);
+    int32_t *s_n = s_meta + 2 * kSlots + 5, *s_list = s_n + 3;             // [width]
+    if (TMA && threadIdx.x == 0) {
+        rr::tc::mbar_init(&full[0], 1);
+        rr::tc::mbar_init(&full[1], 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
 
     const Unit u = unit_of(p, blockIdx.x);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -80,8 +135,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
     const T *k = static_cast<const T *>(p.a.k) + u.b * p.c.k_stride[0] + u.kv_head * p.c.k_stride[1];
     const T *v = static_cast<const T *>(p.a.v) + u.b * p.c.v_stride[0] + u.kv_head * p.c.v_stride[1];
     const uint32_t sk0 = smem_u32(s_k), sv0 = smem_u32(s_v);
-    if (n_tiles > 0) stage_tile<T, DH>(p, u, s_list, slots, 0, k, v, sk0, sv0, s_meta);
-    cp_async_commit();
+    const bool docs = p.a.doc_q != nullptr, bias = p.a.slopes != nullptr, cap = p.c.soft_cap > 0.f;
+    auto stage = [&](int e) {
+        const uint32_t at = (uint32_t)((e & 1) * S::kTile) * 2;
+        if constexpr (TMA) {
+            if (warp == 0) stage_tile_tma<DH>(p, u, maps, s_list, slots, e, sk0 + at, sv0 + at, &full[e & 1]);
+        } else {
+            stage_tile<T, DH>(p, u, s_list, slots, e, k, v, sk0 + at, sv0 + at);
+        }
+        if (docs) stage_documents(p, u, s_list, slots, e, s_meta + (e & 1) * kSlots);
+    };
+    if (n_tiles > 0) stage(0);
+    if constexpr (!TMA) cp_async_commit();
 
     // This lane's two rows.  The 16 rows of a warp belong to one head (chunks
     // are multiples of 16); rows past the unit or past its tokens are computed
@@ -106,7 +171,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
             qf[kk][3] = ok1 ? q1[kk * 8 + 4 + t] : 0u;
         }
     }
-    const bool docs = p.a.doc_q != nullptr, bias = p.a.slopes != nullptr, cap = p.c.soft_cap > 0.f;
     int doc0 = -1, doc1 = -1;
     if (docs) {
         const int32_t *dq = p.a.doc_q + (size_t)u.b * p.c.nq_tokens + token;
@@ -137,20 +201,37 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
     for (int nd = 0; nd < DH / 8; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // l: this lane's part
     const int lm_row = lane & 7, lm_mat = lane >> 3;
-    // ldmatrix lanes: row (lane & 7) of matrix (lane >> 3); keys' matrices are
-    // keys 16 np + {0, 0, 8, 8}, dims 16 kk + {0, 8, 0, 8}, the values' the other way round
-    const uint32_t k_lane = (uint32_t)((lm_row + ((lm_mat >> 1) << 3)) * S::kRow + ((lm_mat & 1) << 3)) * 2;
-    const uint32_t v_lane = (uint32_t)((lm_row + ((lm_mat & 1) << 3)) * S::kRow + ((lm_mat >> 1) << 3)) * 2;
+    // ldmatrix lanes: row (lane & 7) of matrix (lane >> 3); the keys' matrices are
+    // keys 16 np + {0, 0, 8, 8}, dims 16 kk + {0, 8, 0, 8}, the values' the other way
+    // round.  Swizzled rows: 16-byte piece c of row r lies at c ^ (r & 7).
+    const int k_row = lm_row + ((lm_mat >> 1) << 3), k_col = lm_mat & 1;
+    const int v_row = lm_row + ((lm_mat & 1) << 3), v_col = lm_mat >> 1;
+    auto at_k = [&](int np, int kk) {
+        if constexpr (TMA)
+            return (uint32_t)((kk >> 2) * S::kSub * 2 + np * 16 * 128 + k_row * 128 + ((((kk & 3) * 2 + k_col) ^ lm_row) << 4));
+        else
+            return (uint32_t)((np * 16 + k_row) * S::kRow + kk * 16 + k_col * 8) * 2;
+    };
+    auto at_v = [&](int kk, int dp) {
+        if constexpr (TMA)
+            return (uint32_t)((dp >> 2) * S::kSub * 2 + kk * 16 * 128 + v_row * 128 + ((((dp & 3) * 2 + v_col) ^ lm_row) << 4));
+        else
+            return (uint32_t)((kk * 16 + v_row) * S::kRow + dp * 16 + v_col * 8) * 2;
+    };
+    bool ok = true;       // (TMA) no wait has run out
 
     for (int e = 0; e < n_tiles; ++e) {
         const int st = e & 1;
-        if (e + 1 < n_tiles)
-            stage_tile<T, DH>(p, u, s_list, slots, e + 1, k, v, sk0 + (st ^ 1) * S::kTile * 2, sv0 + (st ^ 1) * S::kTile * 2,
-                              s_meta + (st ^ 1) * kSlots);
-        cp_async_commit();
-        cp_async_wait_one();
-        __syncthreads();
-        const uint32_t sk = sk0 + st * S::kTile * 2 + k_lane, sv = sv0 + st * S::kTile * 2 + v_lane;
+        if (e + 1 < n_tiles) stage(e + 1);
+        if constexpr (TMA) {
+            ok = rr::tc::mbar_wait_warp(&full[st], (e >> 1) & 1, abort_flag) && ok;
+            if (docs) __syncthreads();        // the documents
+        } else {
+            cp_async_commit();
+            cp_async_wait_one();
+            __syncthreads();
+        }
+        const uint32_t sk = sk0 + st * S::kTile * 2, sv = sv0 + st * S::kTile * 2;
 
         float s[kSlots / 8][4];
 #pragma unroll
@@ -160,7 +241,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
 #pragma unroll
             for (int np = 0; np < kSlots / 16; ++np) {
                 uint32_t b0, b1, b2, b3;
-                ldmatrix_x4(sk + (np * 16 * S::kRow + kk * 16) * 2, b0, b1, b2, b3);
+                ldmatrix_x4(sk + at_k(np, kk), b0, b1, b2, b3);
                 Half<T>::mma(s[2 * np], qf[kk], b0, b1);
                 Half<T>::mma(s[2 * np + 1], qf[kk], b2, b3);
             }
@@ -264,7 +345,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
 #pragma unroll
             for (int dp = 0; dp < DH / 16; ++dp) {
                 uint32_t b0, b1, b2, b3;
-                ldmatrix_x4_trans(sv + (kk * 16 * S::kRow + dp * 16) * 2, b0, b1, b2, b3);
+                ldmatrix_x4_trans(sv + at_v(kk, dp), b0, b1, b2, b3);
                 Half<T>::mma(o[2 * dp], pa, b0, b1);
                 Half<T>::mma(o[2 * dp + 1], pa, b2, b3);
             }
@@ -272,10 +353,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
         __syncthreads();   // every warp is done with this stage before it is refilled
     }
 
+    if (TMA && !ok) {
+        // the copies in flight land before the block leaves
+        for (int e = max(0, n_tiles - 2); e < n_tiles; ++e) {
+            const long long t0 = clock64();
+            while (!rr::tc::mbar_test(&full[e & 1], (e >> 1) & 1) && clock64() - t0 < rr::tc::kSpinLimit) {
+            }
+        }
+    }
     l0 += __shfl_xor_sync(kFull, l0, 1);
     l0 += __shfl_xor_sync(kFull, l0, 2);
     l1 += __shfl_xor_sync(kFull, l1, 1);
     l1 += __shfl_xor_sync(kFull, l1, 2);
+    if (!ok) l0 = l1 = NAN;
     const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
     bool bad0 = false, bad1 = false;
 #pragma unroll
@@ -309,17 +399,29 @@ __global__ void __launch_bounds__(32 * kMaxWarps, Shape<DH>::kMinBlocks) masked_
     }
 }
 
-template <typename T, int DH>
-cudaError_t launch(const Masked &p, unsigned units, cudaStream_t s) {
-    using S = Shape<DH>;
-    auto kern = masked_attention_kernel<T, DH>;
-    const int list = 16 + 4 * p.c.width;
+template <typename T, int DH, bool TMA>
+cudaError_t launch(const Masked &p, const TileMaps &maps, unsigned units, cudaStream_t s) {
+    using S = Shape<DH, TMA>;
+    auto kern = masked_attention_kernel<T, DH, TMA>;
+    const int list = 4 * p.c.width;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem + 16 + 4 * kMaxWidth, done);
+    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem + 4 * kMaxWidth, done);
     if (e != cudaSuccess) return e;
     const int warps = min(kMaxWarps, (p.group << p.shift) / 16);
-    kern<<<units * (unsigned)p.tiles, 32 * warps, S::kSmem + list, s>>>(p);
+    kern<<<units * (unsigned)p.tiles, 32 * warps, S::kSmem + list, s>>>(p, maps);
     return cudaGetLastError();
+}
+
+template <typename T, int DH>
+cudaError_t launch_small(const Masked &p, unsigned units, cudaStream_t s) {
+    const rr_masked_attn_config &c = p.c;
+    TileMaps maps;
+    const int box = c.chunk < 64 ? c.chunk : 64;
+    if ((long long)units * c.width * c.chunk >= kTmaSlots &&
+        tensor_map(p, p.a.k, c.nk_tokens, c.kv_heads, c.k_stride, box, &maps.k, &maps.axes[0]) &&
+        tensor_map(p, p.a.v, c.nk_tokens, c.kv_heads, c.v_stride, box, &maps.v, &maps.axes[1]))
+        return launch<T, DH, true>(p, maps, units, s);
+    return launch<T, DH, false>(p, maps, units, s);
 }
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -384,12 +486,11 @@ extern "C" rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const
     p.tiles = ((p.group << p.shift) + 16 * kMaxWarps - 1) / (16 * kMaxWarps);
     const unsigned units = (unsigned)((long long)cfg->batch * cfg->route_heads * p.nqc);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (tc_takes(p))
-        e = launch_tc(p, units, s);
-    else if (cfg->dtype == RR_BF16)
-        e = cfg->dh == 64 ? launch<__nv_bfloat16, 64>(p, units, s) : launch<__nv_bfloat16, 128>(p, units, s);
+    cudaError_t e = launch_tc(p, units, s);
+    if (e != cudaErrorNotSupported) return e == cudaSuccess ? RR_OK : RR_ECUDA;
+    if (cfg->dtype == RR_BF16)
+        e = cfg->dh == 64 ? launch_small<__nv_bfloat16, 64>(p, units, s) : launch_small<__nv_bfloat16, 128>(p, units, s);
     else
-        e = cfg->dh == 64 ? launch<__half, 64>(p, units, s) : launch<__half, 128>(p, units, s);
+        e = cfg->dh == 64 ? launch_small<__half, 64>(p, units, s) : launch_small<__half, 128>(p, units, s);
     return e == cudaSuccess ? RR_OK : RR_ECUDA;
 }

@@ -7,6 +7,7 @@
 // numbered head * chunk + token.  All of its rows read the same key chunks.
 #pragma once
 
+#include <cuda.h>
 #include <limits.h>
 #include <math.h>
 
@@ -237,8 +238,13 @@ __device__ __noinline__ void row_alone(const Masked &p, const Unit &u, const int
     for (int e = 0; e < E; ++e) out[e] = Half<T>::down(l == 0.f ? 0.f : o[e] / l);
 }
 
-// The kernel on tcgen05 (rr_masked_tc.cu): whether it takes the problem, and its launch.
-bool tc_takes(const Masked &p);
+// Tensor map of [batch, heads, tokens, dh] by strides, in boxes of tokens by 64
+// elements (rr_masked_tc.cu); false where these strides have none.
+bool tensor_map(const Masked &p, const void *x, int tokens, int heads, const int64_t (&stride)[3], int box_tokens,
+                CUtensorMap *map, int *axes);
+
+// The kernel on tcgen05 (rr_masked_tc.cu); cudaErrorNotSupported, and nothing
+// launched, for problems that are not for it.
 cudaError_t launch_tc(const Masked &p, unsigned units, cudaStream_t s);
 
 }  // namespace rr_masked

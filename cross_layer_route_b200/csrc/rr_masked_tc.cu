@@ -197,9 +197,10 @@ __device__ __forceinline__ Row row_of(const Masked &p, const Unit &u) {
     return r;
 }
 
-// CAP and BIAS: whether the scores are capped and have a bias (each keeps registers
-// and branches out of the loop of the others: 1.09 -> XXX ms for 65536 tokens of 16
-// heads without them).
+// CAP and BIAS: whether the scores are capped and have a bias.  Each keeps its
+// registers and branches out of the others' loop: 1.15 -> 1.01 ms for 65536 tokens
+// of 16 heads without either, 0.51 -> 0.35 ms for 2 x 2048 tokens of 32 heads with a
+// cap (its polynomial in paired operations).
 template <typename T, int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kTcThreads, 1)
 masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_constant__ Maps maps, int items) {
@@ -627,13 +628,15 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     }
 }
 
-// [batch, heads, tokens, dh] by strides, in boxes of tokens by 64 elements.
 // An axis that repeats one row (stride 0) has size 1 in the map; bits 0 and 1 of
-// `axes` say whether the head and the batch entry are coordinates.
-bool tensor_map(const Masked &p, const void *x, int tokens, int heads, const int64_t (&stride)[3], int box_tokens,
+// `axes` say whether the head and the batch entry are coordinates.  Tokens have to
+// be apart, and strides below the map's 2^40 bytes.
+bool tensor_map(const Masked &p, const void *base, int tokens, int heads, const int64_t (&stride)[3], int box_tokens,
                 CUtensorMap *map, int *axes) {
     EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
+    if (!enc || tokens < 1 || (tokens > 1 && stride[2] == 0)) return false;
+    for (int64_t x : stride)
+        if (x >= 1ll << 39) return false;
     const int sizes[2] = {heads, p.c.batch};
     cuuint64_t dims[4] = {(cuuint64_t)p.c.dh, (cuuint64_t)tokens, 1, 1}, bytes[3];
     const cuuint64_t row = (cuuint64_t)p.c.dh * 2;
@@ -650,21 +653,9 @@ bool tensor_map(const Masked &p, const void *x, int tokens, int heads, const int
     }
     const cuuint32_t box[4] = {64u, (cuuint32_t)box_tokens, 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
     return enc(map, p.c.dtype == RR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-               const_cast<void *>(x), dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               const_cast<void *>(base), dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Units that fill a tile of 128 rows; operands whose tokens are apart (a map has
-// no stride of 0 there) and within the map's strides.
-bool tc_takes(const Masked &p) {
-    if ((p.group << p.shift) < kTileRows || p.c.nk_tokens < 1 || p.c.width < 1) return false;
-    if (p.c.nk_tokens > 1 && (p.c.k_stride[2] == 0 || p.c.v_stride[2] == 0)) return false;
-    if (p.c.nq_tokens > 1 && p.c.q_stride[2] == 0) return false;
-    for (const int64_t (*s)[3] : {&p.c.q_stride, &p.c.k_stride, &p.c.v_stride})
-        for (int64_t x : *s)
-            if (x >= 1ll << 39) return false;
-    return true;
 }
 
 template <typename T, int DH, bool CAP, bool BIAS>
@@ -676,7 +667,7 @@ cudaError_t launch_tc_as(const Masked &p, unsigned units, cudaStream_t s) {
     if (!tensor_map(p, p.a.q, c.nq_tokens, c.q_heads, c.q_stride, c.chunk, &maps.q, &maps.axes[0]) ||
         !tensor_map(p, p.a.k, c.nk_tokens, c.kv_heads, c.k_stride, c.chunk, &maps.k, &maps.axes[1]) ||
         !tensor_map(p, p.a.v, c.nk_tokens, c.kv_heads, c.v_stride, c.chunk, &maps.v, &maps.axes[2]))
-        return cudaErrorInvalidValue;
+        return cudaErrorNotSupported;
     auto kern = masked_attention_tc_kernel<T, DH, CAP, BIAS>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem, done);
@@ -695,7 +686,10 @@ cudaError_t launch_tc_type(const Masked &p, unsigned units, cudaStream_t s) {
     return bias ? launch_tc_as<T, DH, false, true>(p, units, s) : launch_tc_as<T, DH, false, false>(p, units, s);
 }
 
+// Units that fill a tile of 128 rows: with fewer, the rows that are missing cost as
+// much as those that are there, and mma.sync, at a quarter of the rate, is as fast.
 cudaError_t launch_tc(const Masked &p, unsigned units, cudaStream_t s) {
+    if ((p.group << p.shift) < kTileRows || p.c.width < 1) return cudaErrorNotSupported;
     if (p.c.dtype == RR_BF16)
         return p.c.dh == 64 ? launch_tc_type<__nv_bfloat16, 64>(p, units, s) : launch_tc_type<__nv_bfloat16, 128>(p, units, s);
     return p.c.dh == 64 ? launch_tc_type<__half, 64>(p, units, s) : launch_tc_type<__half, 128>(p, units, s);

@@ -135,7 +135,11 @@ typedef struct {
 
 /* Enqueues the attention.  Scores, softmax and sums are fp32; the weights are
  * rounded to the inputs' type for the product with v, and the result to that
- * type once.  Errors: RR_EINVAL (shape, stride, null or
+ * type once.  Units of 128 and more rows (q_heads / route_heads * chunk) run on
+ * tcgen05, smaller ones on mma.sync; both give the same bits from call to call.
+ * Rows whose result is not finite take a slow path, key by key.  `out` must not
+ * overlap the inputs.  Every wait inside the kernels is bounded (about a
+ * second); should one run out, the rows not yet written become NaN.  Errors: RR_EINVAL (shape, stride, null or
  * misaligned pointer), RR_ECUDA (launch). */
 rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const rr_masked_attn_args *args,
                               void *stream);

@@ -15,7 +15,9 @@
  * A group with largest magnitude a gets the least exponent e >= -127 with
  * a <= M 2^e; its elements x are stored as x 2^-e rounded to nearest, ties to
  * even, its scale as the byte e + 127.  A group that holds an infinity or a
- * NaN gets the byte 255 and reads back as NaN.
+ * NaN gets the byte 255 and reads back as NaN.  (The format's own NaN codes,
+ * 0x7F and 0xFF, are never stored; in a pool that holds them in places that a
+ * sequence has reached, they can reach query tokens that do not see them.)
  *
  * Conventions of rr.h: device memory is the caller's, a call enqueues on
  * `stream` and returns without synchronising, argument errors come back before
@@ -96,6 +98,9 @@ rr_status rr_cache_read(const rr_cache_config *cfg, const rr_cache_pool *pool, c
  * count once per occurrence).
  *   x = cap * tanh(scale * q.k / cap) - slope_h * (p - s),  o, lse as in rr_attention.h
  * A token with no visible key gets zeros and lse -inf.
+ * Weights are rounded to f16 for the product with the values (below 2^-21 of a
+ * row's largest weight * scale to 2^-32 of it), the result once to dtype; scores,
+ * softmax and sums are fp32.  The same call gives the same bits.
  * Limits: batch, q_tokens >= 0; q_heads a multiple of cache heads, q_heads /
  * heads * q_tokens <= 256; batch * heads <= 65535; table_width * chunk <=
  * 2^24; 0 <= width <= 2^20, route_stride >= max(width, 1); scale >= 0 and at

@@ -229,6 +229,43 @@ def test_two_calls_give_the_same_bits(rr):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("dtype,dh,chunk,hq,hkv,nq,width", [(HF, 64, 32, 8, 8, 1301, 16), (BF, 128, 16, 4, 2, 3300, 24),
+                                                            (BF, 64, 64, 4, 4, 1500, 24), (HF, 128, 16, 16, 16, 700, 20)])
+@pytest.mark.parametrize("kind", ["", "ctsdp"])
+def test_large_calls_equal_their_parts(rr, dtype, dh, chunk, hq, hkv, nq, width, kind):
+    # units of under 128 rows: a large call copies its keys by TMA, its parts by
+    # cp.async, and both compute the same sums in the same order
+    b = 4
+    q, k, v, route = make(b=b, hq=hq, hkv=hkv, nq=nq, dh=dh, chunk=chunk, width=width, dtype=dtype, seed=chunk)
+    kw = masks(kind, b, hq, nq, nq)
+    whole = rr.masked_attention(q, k, v, route, chunk, return_lse=True, **kw)
+    for i in range(b):
+        one = {n: x[i:i + 1].contiguous() if n in ("doc_q", "doc_k", "prefix") else x for n, x in kw.items()}
+        part = rr.masked_attention(q[i:i + 1], k[i:i + 1], v[i:i + 1], route[i:i + 1].contiguous(), chunk, return_lse=True,
+                                   **one)
+        assert torch.equal(whole[0][i:i + 1], part[0]) and torch.equal(whole[1][i:i + 1], part[1])
+    # broadcast keys and values, and rows of several heads side by side
+    wide = torch.randn(b, nq, hkv, 2 * dh, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV).transpose(1, 2)
+    k2, v2 = wide[:1, ..., :dh].expand(b, -1, -1, -1), wide[:, :1, :, dh:].expand(-1, hkv, -1, -1)
+    whole = rr.masked_attention(q, k2, v2, route, chunk, causal=True)
+    part = rr.masked_attention(q, k2.contiguous(), v2.contiguous(), route, chunk, causal=True)
+    assert torch.equal(whole, part)
+
+
+def test_overlapping_and_repeated_rows(rr):
+    # keys that overlap one another (a window over a signal), one key for all tokens, queries likewise
+    for hq, chunk in ((2, 16), (8, 64)):
+        nq, dh = 100, 64
+        _, _, _, route = make(b=1, hq=hq, hkv=2, nq=nq, chunk=chunk)
+        signal = torch.randn(2, nq * 8 + dh, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+        k = signal.as_strided((1, 2, nq, dh), (0, signal.stride(0), 8, 1))
+        v = signal[:, :dh].reshape(1, 2, 1, dh).expand(1, 2, nq, dh)
+        q = signal[:1, :dh].reshape(1, 1, 1, dh).expand(1, hq, nq, dh)
+        for args in ((q, k, k), (q, k, v), (k[:, :1].expand(1, hq, nq, dh), v, k)):
+            got = rr.masked_attention(*args, route, chunk, causal=True, return_lse=True)
+            check(got, *args, route, chunk, causal=True)
+
+
 def test_agrees_with_the_plain_sparse_attention(rr):
     q, k, v, route = make(b=1, hq=4, hkv=4, nq=256, dh=128, chunk=64)
     a = rr.sparse_attention(q[0], k[0], v[0], route[0], 64, causal=True)
