@@ -561,12 +561,29 @@ __global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_a
 
         // scores in base 2 and their masks; c: token g + 8 (c >> 1), row c & 1
         if (cap) {
+            // tanh by its polynomial alone while no score of the warp reaches the cap
+            float most = 0.f;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[u][nt][c] = p.s2 * tanh_f32(s[u][nt][c]);
+                    for (int c = 0; c < 4; ++c) most = fmaxf(most, fabsf(s[u][nt][c]));
+            const bool within = __all_sync(kFull, most < 1.f);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (within) {
+                        tanh_pair(s[u][nt], 1.f);
+                        tanh_pair(s[u][nt] + 2, 1.f);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[u][nt][c] = tanh_f32(s[u][nt][c]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[u][nt][c] *= p.s2;
+                }
         }
         if (bias) {
 #pragma unroll

@@ -99,6 +99,30 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // tanh z.  Up to |z| = 1 z P(z^2), P the polynomial of degree 6 of least largest
 // relative error (5e-8, by exchange in double); beyond that 1 - 2 / (1 + e^2z),
 // where the difference loses no bit.  Relative error below 2^-21 throughout, so a
@@ -116,6 +140,18 @@ __device__ __forceinline__ float tanh_within_one(float z) {
 __device__ __forceinline__ float tanh_f32(float z) {
     const float far = 1.f - __fdividef(2.f, 1.f + ex2(z * 2.8853900817779268f));
     return fabsf(z) < 1.f ? tanh_within_one(z) : far;
+}
+
+// tanh(x s1) of two scores with |x s1| < 1: tanh_within_one, two at a time.
+__device__ __forceinline__ void tanh_pair(float *x, float s1) {
+    const uint64_t z = mul2(pack2(x[0], x[1]), pack2(s1, s1)), y = mul2(z, z);
+    uint64_t s = fma2(y, pack2(0.00104102263f, 0.00104102263f), pack2(-0.00620337910f, -0.00620337910f));
+    s = fma2(y, s, pack2(0.0202899804f, 0.0202899804f));
+    s = fma2(y, s, pack2(-0.0534570296f, -0.0534570296f));
+    s = fma2(y, s, pack2(0.133252041f, 0.133252041f));
+    s = fma2(y, s, pack2(-0.333328392f, -0.333328392f));
+    s = fma2(y, s, pack2(0.99999995f, 0.99999995f));
+    unpack2(mul2(z, s), x[0], x[1]);
 }
 
 // The two 16-bit types of the operators that take either.

@@ -250,11 +250,24 @@ masked_attention_kernel(const __grid_constant__ Masked p, const __grid_constant_
         // Scores in base 2.  Column of s[n][c]: 8n + 2t + (c & 1); row: c >> 1.
         float mul = p.s1;
         if (cap) {
-            mul = 1.f;
+            // tanh by its polynomial alone while no score of the warp reaches the cap
+            mul = p.s2;
+            float most = 0.f;
 #pragma unroll
             for (int n = 0; n < kSlots / 8; ++n)
+                most = fmaxf(most, fmaxf(fmaxf(fabsf(s[n][0]), fabsf(s[n][1])), fmaxf(fabsf(s[n][2]), fabsf(s[n][3]))));
+            if (__all_sync(kFull, most * p.s1 < 1.f)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[n][c] = p.s2 * tanh_f32(s[n][c] * p.s1);
+                for (int n = 0; n < kSlots / 8; ++n) {
+                    tanh_pair(s[n], p.s1);
+                    tanh_pair(s[n] + 2, p.s1);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < kSlots / 8; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[n][c] = tanh_f32(s[n][c] * p.s1);
+            }
         }
         // 16 columns at a time: they are of one chunk
 #pragma unroll

@@ -31,6 +31,10 @@
 namespace rr_masked {
 
 using namespace rr::tc;
+using rr_attn::add2;
+using rr_attn::fma2;
+using rr_attn::pack2;
+using rr_attn::unpack2;
 
 constexpr int kSms = 148;
 constexpr int kTileRows = 128;
@@ -137,41 +141,6 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-    return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t d, float &x, float &y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-// tanh(x s1) of two scores with |x s1| < 1: tanh_within_one, two at a time.
-__device__ __forceinline__ void tanh_pair(float *x, float s1) {
-    const uint64_t z = mul2(pack2(x[0], x[1]), pack2(s1, s1)), y = mul2(z, z);
-    uint64_t s = fma2(y, pack2(0.00104102263f, 0.00104102263f), pack2(-0.00620337910f, -0.00620337910f));
-    s = fma2(y, s, pack2(0.0202899804f, 0.0202899804f));
-    s = fma2(y, s, pack2(-0.0534570296f, -0.0534570296f));
-    s = fma2(y, s, pack2(0.133252041f, 0.133252041f));
-    s = fma2(y, s, pack2(-0.333328392f, -0.333328392f));
-    s = fma2(y, s, pack2(0.99999995f, 0.99999995f));
-    unpack2(mul2(z, s), x[0], x[1]);
 }
 // (NaN if any of them is)
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -326,7 +295,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         const float most = max3(max3(tops[0], tops[1], tops[2]), tops[3], tops[3]);
                         if (__all_sync(kFull, most * p.s1 < 1.f)) {
 #pragma unroll
-                            for (int c = 0; c < kTileKeys; c += 2) tanh_pair(s + c, p.s1);
+                            for (int c = 0; c < kTileKeys; c += 2) rr_attn::tanh_pair(s + c, p.s1);
                         } else {
 #pragma unroll
                             for (int c = 0; c < kTileKeys; ++c) s[c] = rr_attn::tanh_f32(s[c] * p.s1);
