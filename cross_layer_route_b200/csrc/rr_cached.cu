@@ -909,9 +909,15 @@ bool config_ok(const rr_cache_config *c, const rr_cached_attn_config *n) {
     return true;
 }
 
+// Tiles of 8 rows that a CTA takes at once, sharing the codes' conversion.  At dh 128
+// four of them fill the registers (one CTA per SM either way), so two are better
+// where four would stand half empty or few CTAs leave the SMs to latency: 16
+// sequences of up to 8000 tokens, 8 heads: 32 rows 148 us by fours and 165 by twos,
+// 40 rows 261 and 211; one such sequence, 32 rows: 39 and 30.
 int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
-    const int rows = n->q_heads / c->heads * n->q_tokens;
-    return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    const int rows = n->q_heads / c->heads * n->q_tokens, twos = (rows + 15) / 16;
+    if (rows <= 16) return rows <= 8 ? 1 : 2;
+    return c->dh == 64 || (twos % 2 == 0 && (long long)n->batch * c->heads * twos > 148) ? 4 : 2;
 }
 
 // CTAs that share a sequence's tokens, and how their results are joined.  A CTA

@@ -244,6 +244,7 @@ def check(got, codes, scales, fmt, q, lens, table, route=None, **kw):
 ATTN = [dict(), dict(fmt="e2m1"), dict(lens=[1, 16, 17], dh=128, group=4, heads=1), dict(fmt="e2m1", dh=128, group=4, qt=3),
         dict(lens=[2, 130, 0, 64], qt=4, group=8, heads=2, chunk=64, dtype=HF), dict(lens=[700], dh=128, group=1, chunk=128),
         dict(lens=[900, 3], fmt="e2m1", dh=128, group=16, heads=1, chunk=32), dict(lens=[100, 40], dh=128, qt=9, group=4, chunk=32),
+        dict(lens=[33] * 20, heads=4, group=8, qt=4, dh=128), dict(lens=[20, 40] * 10, heads=4, group=8, qt=4, dh=128, fmt="e2m1"),
         dict(lens=[260], heads=1, group=12, qt=7, fmt="e2m1", dtype=HF), dict(lens=[3000, 1500], heads=1, group=3, chunk=64, dh=128)]
 
 
