@@ -1,15 +1,14 @@
 // rr_cached.cu -- attention of a sequence's newest tokens over the paged cache
 // (declared in include/rr_cache.h).
 //
-// A CTA takes a share of one sequence's tokens for one key head and up to 8 NT
-// rows (query token, query head) that read it; its warps take 16 tokens at a
-// time in turn, each with its own running softmax, so nothing in the loop waits
-// for another warp.  Both products put the cache on the 16-row side of
-// mma.sync m16n8k16, where none of it is wasted on padding, and take it straight
-// from global memory:
-//   S^T = K Q^T   A = 16 tokens x 16 dims.  A lane's 16-byte load of a token's
-//                 row holds dims that need not be the ones of the standard
-//                 fragment: the query fragments use the same order.
+// A CTA takes some of one sequence's tokens (cut_of says how many) for one key head
+// and up to 8 NT rows (query token, query head) that read it; its warps take pairs
+// of 16 tokens in turn, each with its own running softmax, so nothing in the loop
+// waits for another warp.  Both products put the cache on the 16-row side of
+// mma.sync m16n8k16, where none of it is wasted on padding:
+//   S^T = K Q^T   A = 16 tokens x 16 dims.  A lane's 16-byte read of a token's row
+//                 holds dims that need not be the ones of the standard fragment:
+//                 the query fragments use the same order.
 //   O^T = V^T P^T A = 16 dims x 16 tokens.  A lane holds 4 tokens' bytes of the
 //                 same dims; bytes of two tokens are paired with prmt.
 // Codes become f16 exactly.  The scales are powers of two: a row's goes to its
@@ -23,7 +22,17 @@
 // of the scores: a score of 2^24 or more would swallow a scale added to it.
 // The references move only when a score passes them by 2^8: most steps then
 // cost one vote and no shuffles.
-// A warp copies its steps (cp.async) into a ring of its own, two or three ahead.
+// A warp copies its steps (cp.async) into a ring of its own, one or two pairs ahead.
+//
+// Measured on a B200: 64 sequences of up to 12001 tokens (8 heads of 128, 4 queries
+// each, e4m3, 1.06 GB of cache) 217 us, 4.9 TB/s of the 6.5 a copy reaches.  The
+// memory alone would take 164 us, the loop without its copies 150: the 64
+// conversions and 50 shifts and permutations that a step of 16 tokens needs share
+// one half-rate pipe, which is busy half of the time.  In 4 bits a step has half
+// the bytes and more of those (scales of 32 elements), so there the pipe is the
+// bound: 16 sequences of 128 routed chunks of 64 tokens, 142 MB, 72 us.  Measured
+// and not kept: 16 warps with single steps (237 us), shifts as products' upper
+// halves on the other pipe (223 us, in 4 bits 12 % slower), two sums per score.
 #include <cooperative_groups.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -50,16 +59,25 @@ constexpr int kState = 4;        // floats beside a partial row: max, sum, value
 // CTAs per SM: what 128 O values a thread and the other fragments leave room for.
 constexpr int ctas_per_sm(int dh, int nt) { return nt * dh <= 128 ? 2 : 1; }
 
+// How the work is cut.  A job is a sequence's tokens for a key head and a row block.
+// kOne: a CTA takes a job.  kCluster: a cluster of CTAs takes a job, kSplits: so do
+// CTAs that leave their parts in the workspace.  kShares: all jobs' steps, laid end
+// to end, are cut into equal shares, one per CTA; a share ends in the middle of a
+// job and may hold several.
+enum { kOne, kCluster, kSplits, kShares };
+constexpr int kMaxShared = 512;  // sequences of a call cut into shares
+
 struct Cached {
     rr_cache_config c;
     rr_cache_pool pool;
     rr_cached_attn_config n;
     rr_cached_attn_args a;
-    float *part;       // [batch * heads, splits, rows, dh + kState], without a cluster
+    float *part;       // [parts, 8 NT rows, dh + kState], with splits or shares
     int shift;         // log2(chunk)
     int group, rows;   // query heads per key head, rows per key head
-    int splits;
-    bool cluster;      // the splits are a cluster of blocks
+    int mode;
+    int blocks;        // CTAs that share a job (cluster, splits), or all jobs (shares)
+    int zs;            // row blocks of 8 NT rows per key head
     float s1, s2;      // as in the masked attention
 };
 
@@ -239,6 +257,34 @@ __device__ __forceinline__ int query_shift(unsigned amax_bits) {
     return e == 0 || e == 255 ? 0 : 13 - (e - 127);
 }
 
+// Steps of 16 tokens of a sequence.
+__device__ __forceinline__ int steps_of(const Cached &p, int b) {
+    const int len = p.a.seq_lens[b];
+    const int entries = len <= 0 ? 0 : p.a.route ? p.n.width : min(p.n.table_width, ((len - 1) >> p.shift) + 1);
+    return entries << (p.shift - 4);
+}
+
+// prefix[i] = steps of the sequences before i, for i in [0, batch], by the block.
+__device__ __forceinline__ void sum_steps(const Cached &p, int *prefix) {
+    for (int i = threadIdx.x; i < p.n.batch; i += blockDim.x) prefix[1 + i] = steps_of(p, i);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int sum = 0;
+        for (int i = threadIdx.x; i - (int)threadIdx.x < p.n.batch; i += 32) {
+            int x = i < p.n.batch ? prefix[1 + i] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, d);
+                if ((int)threadIdx.x >= d) x += y;
+            }
+            if (i < p.n.batch) prefix[1 + i] = sum + x;
+            sum += __shfl_sync(kFull, x, 31);
+        }
+        if (threadIdx.x == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+}
+
 // Two dims of one row's result from its sums: o relative to 2^(n2 - kLift) of the
 // weights', their sum to 2^n1; dim 0's caller writes lse.
 template <int DH>
@@ -264,7 +310,8 @@ __host__ __device__ constexpr int joined_bytes() {
 }
 
 template <int FMT, int DH, int NT>
-__global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_attention_kernel(const __grid_constant__ Cached p) {
+__global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT))
+cached_attention_kernel(const __grid_constant__ Cached p) {
     using W = Words<FMT, DH>;
     constexpr int kRows = 8 * NT, kQRow = DH + 4;      // padded query rows: lanes 8 banks apart
     constexpr int kMT = DH / 16;                       // 16-dim tiles of the values
@@ -279,585 +326,643 @@ __global__ void __launch_bounds__(32 * kAttnWarps, ctas_per_sm(DH, NT)) cached_a
     float *s_part = reinterpret_cast<float *>(s_ring + joined_bytes<FMT, DH, NT>());  // [kRows][DH + kState]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int head = blockIdx.y % p.c.heads, b = blockIdx.y / p.c.heads, row0 = blockIdx.z * kRows;
-    const int len = p.a.seq_lens[b];
-    const int32_t *table = p.a.page_table + (size_t)b * p.n.table_stride;
-    const int32_t *route = p.a.route ? p.a.route + ((size_t)b * p.c.heads + head) * p.n.route_stride : nullptr;
-    const int entries = len <= 0 ? 0 : route ? p.n.width : min(p.n.table_width, ((len - 1) >> p.shift) + 1);
+    int *s_prefix = reinterpret_cast<int *>(s_part + kRows * (DH + kState));          // [batch + 1], with shares
+    long long cur = 0, stop = 0;                       // this share, in steps of all jobs
+    if (p.mode == kShares) {
+        sum_steps(p, s_prefix);
+        const long long total = (long long)s_prefix[p.n.batch] * p.c.heads * p.zs;
+        cur = total * blockIdx.x / p.blocks;
+        stop = total * (blockIdx.x + 1) / p.blocks;
+        if (cur >= stop) return;
+    }
     const int sub_shift = p.shift - 4;                 // steps per chunk
-    const long long all = (long long)entries << sub_shift;
-    const int begin = (int)(all * blockIdx.x / p.splits), end = (int)(all * (blockIdx.x + 1) / p.splits);
+    for (;;) {
+        int head, b, row0, begin, end, job = 0;
+        if (p.mode == kShares) {
+            // the job that step `cur` is in: heads and row blocks of sequence b one after another
+            const int hz = p.c.heads * p.zs;
+            int lo = 0, hi = p.n.batch - 1;                // the last b whose first step is not behind cur
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if ((long long)s_prefix[mid] * hz <= cur) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            const int steps = s_prefix[b + 1] - s_prefix[b];
+            const long long off = cur - (long long)s_prefix[b] * hz;
+            const int in_b = (int)(off / steps);
+            begin = (int)(off % steps);
+            end = (int)min((long long)steps, begin + (stop - cur));
+            head = in_b / p.zs;
+            row0 = in_b % p.zs * kRows;
+            job = b * hz + in_b;
+        } else {
+            head = blockIdx.y % p.c.heads;
+            b = blockIdx.y / p.c.heads;
+            row0 = blockIdx.z * kRows;
+            // (the grid: blocks of a job, sequences and heads, row blocks)
+            job = (blockIdx.y * p.zs + blockIdx.z) * p.blocks;
+            const long long all = steps_of(p, b);
+            begin = (int)(all * blockIdx.x / gridDim.x);
+            end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+        }
+        const int len = p.a.seq_lens[b];
+        const int32_t *table = p.a.page_table + (size_t)b * p.n.table_stride;
+        const int32_t *route = p.a.route ? p.a.route + ((size_t)b * p.c.heads + head) * p.n.route_stride : nullptr;
+        const int entries = len <= 0 ? 0 : route ? p.n.width : min(p.n.table_width, ((len - 1) >> p.shift) + 1);
 
-    // A warp takes pairs of steps, begin + 2 warp on and every 2 kAttnWarps after
-    // that; lane i looks up the page of the i-th of 32 steps.
-    const int mine = begin + 2 * warp < end ? (end - begin - 2 * warp + 2 * kAttnWarps - 1) / (2 * kAttnWarps) : 0;
-    int pos_l = -1;
-    size_t row_l = 0;
-    const uint32_t ring = smem_u32(s_ring) + warp * W::kRing;
-    uint32_t fill = ring;                              // the pair filled next
-    const int first_row = lane / (W::kRowBytes / 16), first_piece = lane % (W::kRowBytes / 16);
-    const uint32_t kat = piece_at<W::kRowBytes, false>(first_row, first_piece);
-    const uint32_t vat = piece_at<W::kRowBytes, true>(first_row, first_piece);
-    int queue[W::kPairs][2];                           // positions of the steps in flight, oldest first
-    auto fetch = [&](int i) {
-        if (i < mine) {
-            if ((i & 15) == 0) {
-                pos_l = -1;
-                row_l = 0;
-                const int step = begin + 2 * (warp + (i + (lane >> 1)) * kAttnWarps) + (lane & 1);
-                if (step < end) {
-                    const int entry = step >> sub_shift;
-                    const int id = route ? route[entry] : entry;
-                    if (id >= 0 && id < p.n.table_width) {
-                        const int at = (id << p.shift) + ((step & ((1 << sub_shift) - 1)) << 4);
-                        const int page = at < len ? table[id] : -1;
-                        if (page >= 0 && page < p.c.pages) {
-                            pos_l = at;
-                            row_l = ((size_t)page * p.c.heads + head) * 2 * p.c.chunk + (at & (p.c.chunk - 1));
+        // A warp takes pairs of steps, begin + 2 warp on and every 2 kAttnWarps after
+        // that; lane i looks up the page of the i-th of 32 steps.
+        const int mine = begin + 2 * warp < end ? (end - begin - 2 * warp + 2 * kAttnWarps - 1) / (2 * kAttnWarps) : 0;
+        int pos_l = -1;
+        size_t row_l = 0;
+        const uint32_t ring = smem_u32(s_ring) + warp * W::kRing;
+        uint32_t fill = ring;                              // the pair filled next
+        const int first_row = lane / (W::kRowBytes / 16), first_piece = lane % (W::kRowBytes / 16);
+        const uint32_t kat = piece_at<W::kRowBytes, false>(first_row, first_piece);
+        const uint32_t vat = piece_at<W::kRowBytes, true>(first_row, first_piece);
+        int queue[W::kPairs][2];                           // positions of the steps in flight, oldest first
+        auto fetch = [&](int i) {
+            if (i < mine) {
+                if ((i & 15) == 0) {
+                    pos_l = -1;
+                    row_l = 0;
+                    const int step = begin + 2 * (warp + (i + (lane >> 1)) * kAttnWarps) + (lane & 1);
+                    if (step < end) {
+                        const int entry = step >> sub_shift;
+                        const int id = route ? route[entry] : entry;
+                        if (id >= 0 && id < p.n.table_width) {
+                            const int at = (id << p.shift) + ((step & ((1 << sub_shift) - 1)) << 4);
+                            const int page = at < len ? table[id] : -1;
+                            if (page >= 0 && page < p.c.pages) {
+                                pos_l = at;
+                                row_l = ((size_t)page * p.c.heads + head) * 2 * p.c.chunk + (at & (p.c.chunk - 1));
+                            }
                         }
                     }
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int from = 2 * (i & 15) + u;
-                const int pos = __shfl_sync(kFull, pos_l, from);
-                const size_t row = __shfl_sync(kFull, row_l, from);
-                queue[W::kPairs - 1][u] = pos;
-                copy_step<FMT, DH>(fill + u * W::kStage, kat, vat, p, row, pos, len);
-            }
-            fill = fill == ring + W::kRing - 2 * W::kStage ? ring : fill + 2 * W::kStage;
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < W::kPairs - 1; ++i) {
-        fetch(i);
-        queue[i][0] = queue[W::kPairs - 1][0];
-        queue[i][1] = queue[W::kPairs - 1][1];
-    }
-
-    // queries: eight lanes a row, DH / 8 elements each
-    for (int r = warp * 4 + lane / 8; r < kRows; r += kAttnWarps * 4) {
-        const int row = row0 + r, at8 = (lane & 7) * (DH / 8);
-        float x[DH / 8];
-        unsigned amax = 0;
-#pragma unroll
-        for (int i = 0; i < DH / 8; i += 8) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (row < p.rows) {
-                const int64_t at = b * p.n.q_stride[0] + (row / p.group) * p.n.q_stride[1] +
-                                   (head * p.group + row % p.group) * p.n.q_stride[2] + at8 + i;
-                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.a.q) + at));
-            }
-            const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = p.n.dtype == RR_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h[e]))
-                                                      : __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-                x[i + 2 * e] = f.x;
-                x[i + 2 * e + 1] = f.y;
-                amax = max(amax, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-            }
-        }
-        const unsigned group_mask = 0xffu << (lane & 24);
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) amax = max(amax, __shfl_xor_sync(group_mask, amax, d));
-        const int shift = query_shift(amax);
-        // 2^shift in two factors: a shift can be as large as 162
-        const float half0 = __uint_as_float((unsigned)(127 + shift / 2) << 23);
-        const float half1 = __uint_as_float((unsigned)(127 + shift - shift / 2) << 23);
-#pragma unroll
-        for (int i = 0; i < DH / 8; i += 2)
-            *reinterpret_cast<uint32_t *>(s_q + r * kQRow + at8 + i) = pack_f16(x[i] * half0 * half1, x[i + 1] * half0 * half1);
-        if ((lane & 7) == 0) s_row[r] = ldexpf(p.s1, -shift);
-    }
-    // The distance that the bias is taken relative to: the newest token's to the
-    // nearest key that has a page (see `nearest` of the masked attention).
-    if (warp == 0) {
-        int best = INT_MAX;
-        if (p.a.slopes && len > 0) {
-            for (int e0 = 0; e0 < entries; e0 += 32) {
-                const int e = e0 + lane;
-                if (e < entries) {
-                    const int id = route ? route[e] : entries - 1 - e;
-                    if (id >= 0 && id < p.n.table_width && (id << p.shift) < len) {
-                        const int page = table[id];
-                        if (page >= 0 && page < p.c.pages)
-                            best = min(best, max(0, len - 1 - ((id << p.shift) + p.c.chunk - 1)));
-                    }
+                for (int u = 0; u < 2; ++u) {
+                    const int from = 2 * (i & 15) + u;
+                    const int pos = __shfl_sync(kFull, pos_l, from);
+                    const size_t row = __shfl_sync(kFull, row_l, from);
+                    queue[W::kPairs - 1][u] = pos;
+                    copy_step<FMT, DH>(fill + u * W::kStage, kat, vat, p, row, pos, len);
                 }
-                if (!route && __any_sync(kFull, best != INT_MAX)) break;   // entries come nearest first
+                fill = fill == ring + W::kRing - 2 * W::kStage ? ring : fill + 2 * W::kStage;
             }
-            best = __reduce_min_sync(kFull, best);
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < W::kPairs - 1; ++i) {
+            fetch(i);
+            queue[i][0] = queue[W::kPairs - 1][0];
+            queue[i][1] = queue[W::kPairs - 1][1];
         }
-        if (lane == 0) *s_near = best == INT_MAX ? 0 : best;
-    }
-    __syncthreads();
 
-    uint32_t qf[NT <= 2 ? NT : 1][DH / 16][2];
-    auto query = [&](int nt, int j, uint32_t &b0, uint32_t &b1) {
-        const int dim = FMT == RR_E2M1 ? 32 * (j / 2) + 8 * t + 4 * (j % 2) : 64 * (j / 4) + 16 * t + 4 * (j % 4);
-        const uint2 w = *reinterpret_cast<const uint2 *>(s_q + (nt * 8 + g) * kQRow + dim);
-        b0 = w.x;
-        b1 = w.y;
-    };
-    if constexpr (NT <= 2) {
+        // queries: eight lanes a row, DH / 8 elements each
+        for (int r = warp * 4 + lane / 8; r < kRows; r += kAttnWarps * 4) {
+            const int row = row0 + r, at8 = (lane & 7) * (DH / 8);
+            float x[DH / 8];
+            unsigned amax = 0;
+#pragma unroll
+            for (int i = 0; i < DH / 8; i += 8) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (row < p.rows) {
+                    const int64_t at = b * p.n.q_stride[0] + (row / p.group) * p.n.q_stride[1] +
+                                       (head * p.group + row % p.group) * p.n.q_stride[2] + at8 + i;
+                    w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.a.q) + at));
+                }
+                const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = p.n.dtype == RR_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h[e]))
+                                                          : __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+                    x[i + 2 * e] = f.x;
+                    x[i + 2 * e + 1] = f.y;
+                    amax = max(amax, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+                }
+            }
+            const unsigned group_mask = 0xffu << (lane & 24);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) amax = max(amax, __shfl_xor_sync(group_mask, amax, d));
+            const int shift = query_shift(amax);
+            // 2^shift in two factors: a shift can be as large as 162
+            const float half0 = __uint_as_float((unsigned)(127 + shift / 2) << 23);
+            const float half1 = __uint_as_float((unsigned)(127 + shift - shift / 2) << 23);
+#pragma unroll
+            for (int i = 0; i < DH / 8; i += 2)
+                *reinterpret_cast<uint32_t *>(s_q + r * kQRow + at8 + i) = pack_f16(x[i] * half0 * half1, x[i + 1] * half0 * half1);
+            if ((lane & 7) == 0) s_row[r] = ldexpf(p.s1, -shift);
+        }
+        // The distance that the bias is taken relative to: the newest token's to the
+        // nearest key that has a page (see `nearest` of the masked attention).
+        if (warp == 0) {
+            int best = INT_MAX;
+            if (p.a.slopes && len > 0) {
+                for (int e0 = 0; e0 < entries; e0 += 32) {
+                    const int e = e0 + lane;
+                    if (e < entries) {
+                        const int id = route ? route[e] : entries - 1 - e;
+                        if (id >= 0 && id < p.n.table_width && (id << p.shift) < len) {
+                            const int page = table[id];
+                            if (page >= 0 && page < p.c.pages)
+                                best = min(best, max(0, len - 1 - ((id << p.shift) + p.c.chunk - 1)));
+                        }
+                    }
+                    if (!route && __any_sync(kFull, best != INT_MAX)) break;   // entries come nearest first
+                }
+                best = __reduce_min_sync(kFull, best);
+            }
+            if (lane == 0) *s_near = best == INT_MAX ? 0 : best;
+        }
+        __syncthreads();
+
+        uint32_t qf[NT <= 2 ? NT : 1][DH / 16][2];
+        auto query = [&](int nt, int j, uint32_t &b0, uint32_t &b1) {
+            const int dim = FMT == RR_E2M1 ? 32 * (j / 2) + 8 * t + 4 * (j % 2) : 64 * (j / 4) + 16 * t + 4 * (j % 4);
+            const uint2 w = *reinterpret_cast<const uint2 *>(s_q + (nt * 8 + g) * kQRow + dim);
+            b0 = w.x;
+            b1 = w.y;
+        };
+        if constexpr (NT <= 2) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < DH / 16; ++j) query(nt, j, qf[nt][j][0], qf[nt][j][1]);
+        }
+
+        // this lane's rows of every tile of 8: 2t, 2t + 1
+        float rowf[NT][2], slope[NT][2];
+        int pos_r[NT][2], near_r[NT][2];
+        const bool bias = p.a.slopes != nullptr, cap = p.n.soft_cap > 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < DH / 16; ++j) query(nt, j, qf[nt][j][0], qf[nt][j][1]);
-    }
-
-    // this lane's rows of every tile of 8: 2t, 2t + 1
-    float rowf[NT][2], slope[NT][2];
-    int pos_r[NT][2], near_r[NT][2];
-    const bool bias = p.a.slopes != nullptr, cap = p.n.soft_cap > 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = nt * 8 + 2 * t + i, row = row0 + r;
-            const int back = p.n.q_tokens - 1 - (row < p.rows ? row / p.group : 0);   // tokens after it
-            rowf[nt][i] = s_row[r];
-            pos_r[nt][i] = row < p.rows ? len - 1 - back : -1;
-            near_r[nt][i] = max(0, *s_near - back);
-            slope[nt][i] = bias && row < p.rows ? p.a.slopes[head * p.group + row % p.group] * kLog2e : 0.f;
-        }
-
-    float o[kMT][NT][4];
-#pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-    float m1[NT][2], m2[NT][2], l[NT][2];
-    uint32_t broken = 0;    // (row of the lane, group): a visible value's scale is NaN
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m1[nt][0] = m1[nt][1] = m2[nt][0] = m2[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-
-    const unsigned char *stage = s_ring + warp * W::kRing, *last_pair = stage + W::kRing - 2 * W::kStage;
-    const int all_see = len - p.n.q_tokens;            // positions up to here are visible to every row
-    for (int i = 0; i < mine; ++i, stage = stage == last_pair ? stage - (W::kRing - 2 * W::kStage) : stage + 2 * W::kStage) {
-        __syncwarp();     // every lane is done with the pair that is filled now
-        fetch(i + W::kPairs - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(W::kPairs - 1) : "memory");
-        __syncwarp();
-        const int pos[2] = {queue[0][0], queue[0][1]};
-#pragma unroll
-        for (int j = 0; j + 1 < W::kPairs; ++j) queue[j][0] = queue[j + 1][0], queue[j][1] = queue[j + 1][1];
-        if (pos[0] < 0 && pos[1] < 0) continue;
-
-        // S^T: tokens g, g + 8 of each step by rows 2t, 2t + 1
-        float s[2][NT][4];
-        uint32_t vs[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const unsigned char *st = stage + u * W::kStage;
-            uint32_t ks[2], k0[W::kK], k1[W::kK];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ks[h] = read_scales<FMT, DH>(st, 0, g + 8 * h);
-                vs[u][h] = read_scales<FMT, DH>(st, 1, g + 8 * h);
+            for (int i = 0; i < 2; ++i) {
+                const int r = nt * 8 + 2 * t + i, row = row0 + r;
+                const int back = p.n.q_tokens - 1 - (row < p.rows ? row / p.group : 0);   // tokens after it
+                rowf[nt][i] = s_row[r];
+                pos_r[nt][i] = row < p.rows ? len - 1 - back : -1;
+                near_r[nt][i] = max(0, *s_near - back);
+                slope[nt][i] = bias && row < p.rows ? p.a.slopes[head * p.group + row % p.group] * kLog2e : 0.f;
             }
-            read_key<FMT, DH>(k0, st, g, t);
-            read_key<FMT, DH>(k1, st, g + 8, t);
+
+        float o[kMT][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
-            if constexpr (FMT == RR_E4M3) {
+        for (int i = 0; i < kMT; ++i)
 #pragma unroll
-                for (int j = 0; j < DH / 16; ++j) {
-                    const uint32_t a[4] = {f16x2_of_e4m3(k0[j]), f16x2_of_e4m3(k1[j]), f16x2_of_e4m3(k0[j] >> 16),
-                                           f16x2_of_e4m3(k1[j] >> 16)};
+            for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+        float m1[NT][2], m2[NT][2], l[NT][2];
+        uint32_t broken = 0;    // (row of the lane, group): a visible value's scale is NaN
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t b0, b1;
-                        if constexpr (NT <= 2) b0 = qf[nt][j][0], b1 = qf[nt][j][1];
-                        else query(nt, j, b0, b1);
-                        mma_f16(s[u][nt], a, b0, b1);
-                    }
+        for (int nt = 0; nt < NT; ++nt) m1[nt][0] = m1[nt][1] = m2[nt][0] = m2[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+
+        const unsigned char *stage = s_ring + warp * W::kRing, *last_pair = stage + W::kRing - 2 * W::kStage;
+        const int all_see = len - p.n.q_tokens;            // positions up to here are visible to every row
+        for (int i = 0; i < mine; ++i, stage = stage == last_pair ? stage - (W::kRing - 2 * W::kStage) : stage + 2 * W::kStage) {
+            __syncwarp();     // every lane is done with the pair that is filled now
+            fetch(i + W::kPairs - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(W::kPairs - 1) : "memory");
+            __syncwarp();
+            const int pos[2] = {queue[0][0], queue[0][1]};
+#pragma unroll
+            for (int j = 0; j + 1 < W::kPairs; ++j) queue[j][0] = queue[j + 1][0], queue[j][1] = queue[j + 1][1];
+            if (pos[0] < 0 && pos[1] < 0) continue;
+
+            // S^T: tokens g, g + 8 of each step by rows 2t, 2t + 1
+            float s[2][NT][4];
+            uint32_t vs[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const unsigned char *st = stage + u * W::kStage;
+                uint32_t ks[2], k0[W::kK], k1[W::kK];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    ks[h] = read_scales<FMT, DH>(st, 0, g + 8 * h);
+                    vs[u][h] = read_scales<FMT, DH>(st, 1, g + 8 * h);
                 }
-                const float kf[2] = {power_of_two(ks[0]), power_of_two(ks[1])};
+                read_key<FMT, DH>(k0, st, g, t);
+                read_key<FMT, DH>(k1, st, g + 8, t);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+                if constexpr (FMT == RR_E4M3) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[u][nt][c] = s[u][nt][c] * rowf[nt][c & 1] * kf[c >> 1];
-            } else {
-                // each group's part of the score by the group's scale
-#pragma unroll
-                for (int grp = 0; grp < W::kGroups; ++grp) {
-                    float part[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t w0 = k0[grp] >> (16 * j), w1 = k1[grp] >> (16 * j);
-                        const uint32_t a[4] = {f16x2_of_e2m1(w0), f16x2_of_e2m1(w1), f16x2_of_e2m1(w0 >> 8),
-                                               f16x2_of_e2m1(w1 >> 8)};
+                    for (int j = 0; j < DH / 16; ++j) {
+                        const uint32_t a[4] = {f16x2_of_e4m3(k0[j]), f16x2_of_e4m3(k1[j]), f16x2_of_e4m3(k0[j] >> 16),
+                                               f16x2_of_e4m3(k1[j] >> 16)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             uint32_t b0, b1;
-                            if constexpr (NT <= 2) b0 = qf[nt][2 * grp + j][0], b1 = qf[nt][2 * grp + j][1];
-                            else query(nt, 2 * grp + j, b0, b1);
-                            mma_f16(part[nt], a, b0, b1);
+                            if constexpr (NT <= 2) b0 = qf[nt][j][0], b1 = qf[nt][j][1];
+                            else query(nt, j, b0, b1);
+                            mma_f16(s[u][nt], a, b0, b1);
                         }
                     }
-                    const float kf[2] = {power_of_two((ks[0] >> (8 * grp)) & 255), power_of_two((ks[1] >> (8 * grp)) & 255)};
+                    const float kf[2] = {power_of_two(ks[0]), power_of_two(ks[1])};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) s[u][nt][c] = fmaf(part[nt][c], kf[c >> 1], s[u][nt][c]);
-                }
+                        for (int c = 0; c < 4; ++c) s[u][nt][c] = s[u][nt][c] * rowf[nt][c & 1] * kf[c >> 1];
+                } else {
+                    // each group's part of the score by the group's scale
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int grp = 0; grp < W::kGroups; ++grp) {
+                        float part[NT][4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[u][nt][c] *= rowf[nt][c & 1];
-            }
-        }
-
-        // The values' scales: the exponent ev that goes to a token's weight, and with
-        // groups the f16 factors of this lane's dims.  NaN scales and groups 2^26 below
-        // their row's largest are rare, and looked at once per step.
-        float ev[2][2];
-        uint32_t vf[2][2];
+                        for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if constexpr (FMT == RR_E4M3) {
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t w0 = k0[grp] >> (16 * j), w1 = k1[grp] >> (16 * j);
+                            const uint32_t a[4] = {f16x2_of_e2m1(w0), f16x2_of_e2m1(w1), f16x2_of_e2m1(w0 >> 8),
+                                                   f16x2_of_e2m1(w1 >> 8)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) ev[u][h] = vs[u][h] == 255 ? NAN : (float)((int)vs[u][h] - 127);
-            } else {
-                const int grp8 = (DH == 128 ? g / 2 : g / 4) * 8;
-                unsigned top[2] = {top_scale<W::kGroups>(vs[u][0]), top_scale<W::kGroups>(vs[u][1])};
-                const uint32_t both = top[0] | top[1] << 16;
-                const int from = 8 * t;                // the lane of token 2t; of 2t + 1: from + 4
-                const uint32_t w0 = __shfl_sync(kFull, vs[u][0], from), w1 = __shfl_sync(kFull, vs[u][0], from + 4);
-                const uint32_t w2 = __shfl_sync(kFull, vs[u][1], from), w3 = __shfl_sync(kFull, vs[u][1], from + 4);
-                const uint32_t ta = __shfl_sync(kFull, both, from), tb = __shfl_sync(kFull, both, from + 4);
-                const int f0 = (int)((w0 >> grp8) & 255) - (int)(ta & 0xffffu) + kGroupLift + 15;
-                const int f1 = (int)((w1 >> grp8) & 255) - (int)(tb & 0xffffu) + kGroupLift + 15;
-                const int f2 = (int)((w2 >> grp8) & 255) - (int)(ta >> 16) + kGroupLift + 15;
-                const int f3 = (int)((w3 >> grp8) & 255) - (int)(tb >> 16) + kGroupLift + 15;
-                vf[u][0] = (uint32_t)f0 << 10 | (uint32_t)f1 << 26;
-                vf[u][1] = (uint32_t)f2 << 10 | (uint32_t)f3 << 26;
-                if (__any_sync(kFull, min(min(f0, f1), min(f2, f3)) < 1 || max(top[0], top[1]) == 255)) {
+                            for (int nt = 0; nt < NT; ++nt) {
+                                uint32_t b0, b1;
+                                if constexpr (NT <= 2) b0 = qf[nt][2 * grp + j][0], b1 = qf[nt][2 * grp + j][1];
+                                else query(nt, 2 * grp + j, b0, b1);
+                                mma_f16(part[nt], a, b0, b1);
+                            }
+                        }
+                        const float kf[2] = {power_of_two((ks[0] >> (8 * grp)) & 255), power_of_two((ks[1] >> (8 * grp)) & 255)};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int grp = 0; grp < W::kGroups; ++grp)
-                            if (pos[u] >= 0 && ((vs[u][h] >> (8 * grp)) & 255) == 255)
-#pragma unroll
-                                for (int r = 0; r < 2 * NT; ++r)
-                                    if (pos[u] + g + 8 * h <= pos_r[r >> 1][r & 1]) broken |= 1u << (r * W::kGroups + grp);
-                        top[h] = top_number<W::kGroups>(vs[u][h]);
-                    }
-                    vf[u][0] = group_factor((w0 >> grp8) & 255, top_number<W::kGroups>(w0)) |
-                               group_factor((w1 >> grp8) & 255, top_number<W::kGroups>(w1)) << 16;
-                    vf[u][1] = group_factor((w2 >> grp8) & 255, top_number<W::kGroups>(w2)) |
-                               group_factor((w3 >> grp8) & 255, top_number<W::kGroups>(w3)) << 16;
-                }
-                ev[u][0] = (float)((int)top[0] - 127 - kGroupLift);
-                ev[u][1] = (float)((int)top[1] - 127 - kGroupLift);
-            }
-        }
-
-        // scores in base 2 and their masks; c: token g + 8 (c >> 1), row c & 1
-        if (cap) {
-            // tanh by its polynomial alone while no score of the warp reaches the cap
-            float most = 0.f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) most = fmaxf(most, fabsf(s[u][nt][c]));
-            const bool within = __all_sync(kFull, most < 1.f);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (within) {
-                        tanh_pair(s[u][nt], 1.f);
-                        tanh_pair(s[u][nt] + 2, 1.f);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) s[u][nt][c] = tanh_f32(s[u][nt][c]);
+                            for (int c = 0; c < 4; ++c) s[u][nt][c] = fmaf(part[nt][c], kf[c >> 1], s[u][nt][c]);
                     }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[u][nt][c] *= p.s2;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[u][nt][c] *= rowf[nt][c & 1];
                 }
-        }
-        if (bias) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        s[u][nt][c] -= slope[nt][c & 1] *
-                                       (float)(pos_r[nt][c & 1] - near_r[nt][c & 1] - pos[u] - g - 8 * (c >> 1));
-        }
-        if (max(pos[0], pos[1]) + 15 > all_see || min(pos[0], pos[1]) < 0) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (pos[u] < 0 || pos[u] + g + 8 * (c >> 1) > pos_r[nt][c & 1]) s[u][nt][c] = -INFINITY;
-        }
-        // A masked score is -inf: its weights are zero and it moves no reference
-        // whatever its value's scale, a NaN too.
-        const float top_ev = fmaxf(fmaxf(ev[0][0], ev[0][1]), fmaxf(ev[1][0], ev[1][1]));
-        bool grow = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                // (an upper bound of the tokens' sums: at worst a move that was not needed)
-                const float a = fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r]));
-                grow = grow || a - m1[nt][r] > fminf(kSlack, m2[nt][r] + kSlack - top_ev);
             }
-        if (__any_sync(kFull, grow)) {
+
+            // The values' scales: the exponent ev that goes to a token's weight, and with
+            // groups the f16 factors of this lane's dims.  NaN scales and groups 2^26 below
+            // their row's largest are rare, and looked at once per step.
+            float ev[2][2];
+            uint32_t vf[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if constexpr (FMT == RR_E4M3) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) ev[u][h] = vs[u][h] == 255 ? NAN : (float)((int)vs[u][h] - 127);
+                } else {
+                    const int grp8 = (DH == 128 ? g / 2 : g / 4) * 8;
+                    unsigned top[2] = {top_scale<W::kGroups>(vs[u][0]), top_scale<W::kGroups>(vs[u][1])};
+                    const uint32_t both = top[0] | top[1] << 16;
+                    const int from = 8 * t;                // the lane of token 2t; of 2t + 1: from + 4
+                    const uint32_t w0 = __shfl_sync(kFull, vs[u][0], from), w1 = __shfl_sync(kFull, vs[u][0], from + 4);
+                    const uint32_t w2 = __shfl_sync(kFull, vs[u][1], from), w3 = __shfl_sync(kFull, vs[u][1], from + 4);
+                    const uint32_t ta = __shfl_sync(kFull, both, from), tb = __shfl_sync(kFull, both, from + 4);
+                    const int f0 = (int)((w0 >> grp8) & 255) - (int)(ta & 0xffffu) + kGroupLift + 15;
+                    const int f1 = (int)((w1 >> grp8) & 255) - (int)(tb & 0xffffu) + kGroupLift + 15;
+                    const int f2 = (int)((w2 >> grp8) & 255) - (int)(ta >> 16) + kGroupLift + 15;
+                    const int f3 = (int)((w3 >> grp8) & 255) - (int)(tb >> 16) + kGroupLift + 15;
+                    vf[u][0] = (uint32_t)f0 << 10 | (uint32_t)f1 << 26;
+                    vf[u][1] = (uint32_t)f2 << 10 | (uint32_t)f3 << 26;
+                    if (__any_sync(kFull, min(min(f0, f1), min(f2, f3)) < 1 || max(top[0], top[1]) == 255)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int grp = 0; grp < W::kGroups; ++grp)
+                                if (pos[u] >= 0 && ((vs[u][h] >> (8 * grp)) & 255) == 255)
+#pragma unroll
+                                    for (int r = 0; r < 2 * NT; ++r)
+                                        if (pos[u] + g + 8 * h <= pos_r[r >> 1][r & 1]) broken |= 1u << (r * W::kGroups + grp);
+                            top[h] = top_number<W::kGroups>(vs[u][h]);
+                        }
+                        vf[u][0] = group_factor((w0 >> grp8) & 255, top_number<W::kGroups>(w0)) |
+                                   group_factor((w1 >> grp8) & 255, top_number<W::kGroups>(w1)) << 16;
+                        vf[u][1] = group_factor((w2 >> grp8) & 255, top_number<W::kGroups>(w2)) |
+                                   group_factor((w3 >> grp8) & 255, top_number<W::kGroups>(w3)) << 16;
+                    }
+                    ev[u][0] = (float)((int)top[0] - 127 - kGroupLift);
+                    ev[u][1] = (float)((int)top[1] - 127 - kGroupLift);
+                }
+            }
+
+            // scores in base 2 and their masks; c: token g + 8 (c >> 1), row c & 1
+            if (cap) {
+                // tanh by its polynomial alone while no score of the warp reaches the cap
+                float most = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) most = fmaxf(most, fabsf(s[u][nt][c]));
+                const bool within = __all_sync(kFull, most < 1.f);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (within) {
+                            tanh_pair(s[u][nt], 1.f);
+                            tanh_pair(s[u][nt] + 2, 1.f);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) s[u][nt][c] = tanh_f32(s[u][nt][c]);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[u][nt][c] *= p.s2;
+                    }
+            }
+            if (bias) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            s[u][nt][c] -= slope[nt][c & 1] *
+                                           (float)(pos_r[nt][c & 1] - near_r[nt][c & 1] - pos[u] - g - 8 * (c >> 1));
+            }
+            if (max(pos[0], pos[1]) + 15 > all_see || min(pos[0], pos[1]) < 0) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (pos[u] < 0 || pos[u] + g + 8 * (c >> 1) > pos_r[nt][c & 1]) s[u][nt][c] = -INFINITY;
+            }
+            // A masked score is -inf: its weights are zero and it moves no reference
+            // whatever its value's scale, a NaN too.
+            const float top_ev = fmaxf(fmaxf(ev[0][0], ev[0][1]), fmaxf(ev[1][0], ev[1][1]));
+            bool grow = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float a = fmaxf(m1[nt][r], fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r])));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, d));
-                    const float base = a == -INFINITY ? 0.f : a, down = m1[nt][r] - base;
-                    float c = fmaxf(fmaxf(s[0][nt][r] - base + ev[0][0], s[0][nt][2 + r] - base + ev[0][1]),
-                                    fmaxf(s[1][nt][r] - base + ev[1][0], s[1][nt][2 + r] - base + ev[1][1]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) c = fmaxf(c, __shfl_xor_sync(kFull, c, d));
-                    const float was = m2[nt][r] + down;
-                    c = fmaxf(c, was);
-                    l[nt][r] *= ex2(down);
-                    const float corr = c == -INFINITY ? 1.f : ex2(was - c);
-                    m1[nt][r] = a;
-                    m2[nt][r] = c;
-#pragma unroll
-                    for (int i2 = 0; i2 < kMT; ++i2) {
-                        o[i2][nt][r] *= corr;
-                        o[i2][nt][2 + r] *= corr;
-                    }
+                    // (an upper bound of the tokens' sums: at worst a move that was not needed)
+                    const float a = fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r]));
+                    grow = grow || a - m1[nt][r] > fminf(kSlack, m2[nt][r] + kSlack - top_ev);
                 }
-        }
+            if (__any_sync(kFull, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float a = fmaxf(m1[nt][r], fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r])));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, d));
+                        const float base = a == -INFINITY ? 0.f : a, down = m1[nt][r] - base;
+                        float c = fmaxf(fmaxf(s[0][nt][r] - base + ev[0][0], s[0][nt][2 + r] - base + ev[0][1]),
+                                        fmaxf(s[1][nt][r] - base + ev[1][0], s[1][nt][2 + r] - base + ev[1][1]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) c = fmaxf(c, __shfl_xor_sync(kFull, c, d));
+                        const float was = m2[nt][r] + down;
+                        c = fmaxf(c, was);
+                        l[nt][r] *= ex2(down);
+                        const float corr = c == -INFINITY ? 1.f : ex2(was - c);
+                        m1[nt][r] = a;
+                        m2[nt][r] = c;
+#pragma unroll
+                        for (int i2 = 0; i2 < kMT; ++i2) {
+                            o[i2][nt][r] *= corr;
+                            o[i2][nt][2 + r] *= corr;
+                        }
+                    }
+            }
 
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const unsigned char *st = stage + u * W::kStage;
-            // weights: P^T fragments by transposing 8x8 blocks
-            uint32_t pb[NT][2];
+            for (int u = 0; u < 2; ++u) {
+                const unsigned char *st = stage + u * W::kStage;
+                // weights: P^T fragments by transposing 8x8 blocks
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int r = c & 1;
+                        // -inf - -inf: a row that has seen nothing yet
+                        const bool none = s[u][nt][c] == -INFINITY;
+                        const float x = s[u][nt][c] - m1[nt][r];
+                        l[nt][r] += none ? 0.f : ex2(x);
+                        w[c] = none ? 0.f : ex2(x + (ev[u][c >> 1] - m2[nt][r] + kLift));
+                    }
+                    pb[nt][0] = transpose_8x8(pack_f16(w[0], w[1]));
+                    pb[nt][1] = transpose_8x8(pack_f16(w[2], w[3]));
+                }
+
+                // O^T: dims (DH / 8) g + 2 i (rows g) and + 1 (rows g + 8) of tile i
+                uint32_t v[4][W::kV];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) read_value<FMT, DH>(v[q], st, 2 * t + (q & 1) + 8 * (q >> 1), g);
+#pragma unroll
+                for (int j = 0; j < W::kV; ++j) {
+                    if constexpr (FMT == RR_E4M3) {
+                        const uint32_t x0 = __byte_perm(v[0][j], v[1][j], 0x5140), x1 = __byte_perm(v[2][j], v[3][j], 0x5140);
+                        const uint32_t y0 = __byte_perm(v[0][j], v[1][j], 0x7362), y1 = __byte_perm(v[2][j], v[3][j], 0x7362);
+                        const uint32_t a[4] = {f16x2_of_e4m3(x0), f16x2_of_e4m3(x0 >> 16), f16x2_of_e4m3(x1),
+                                               f16x2_of_e4m3(x1 >> 16)};
+                        const uint32_t c[4] = {f16x2_of_e4m3(y0), f16x2_of_e4m3(y0 >> 16), f16x2_of_e4m3(y1),
+                                               f16x2_of_e4m3(y1 >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(o[2 * j][nt], a, pb[nt][0], pb[nt][1]);
+                            mma_f16(o[2 * j + 1][nt], c, pb[nt][0], pb[nt][1]);
+                        }
+                    } else {
+                        // byte i of a row holds dims 2i (low half) and 2i + 1
+                        const uint32_t lo0 = (v[0][j] & 0x0f0f0f0fu) | (v[1][j] & 0x0f0f0f0fu) << 4;
+                        const uint32_t hi0 = ((v[0][j] >> 4) & 0x0f0f0f0fu) | (v[1][j] & 0xf0f0f0f0u);
+                        const uint32_t lo1 = (v[2][j] & 0x0f0f0f0fu) | (v[3][j] & 0x0f0f0f0fu) << 4;
+                        const uint32_t hi1 = ((v[2][j] >> 4) & 0x0f0f0f0fu) | (v[3][j] & 0xf0f0f0f0u);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t a[4] = {mul_f16x2(f16x2_of_e2m1(lo0 >> (8 * q)), vf[u][0]),
+                                                   mul_f16x2(f16x2_of_e2m1(hi0 >> (8 * q)), vf[u][0]),
+                                                   mul_f16x2(f16x2_of_e2m1(lo1 >> (8 * q)), vf[u][1]),
+                                                   mul_f16x2(f16x2_of_e2m1(hi1 >> (8 * q)), vf[u][1])};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * j + q][nt], a, pb[nt][0], pb[nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+
+        // the lanes of a row's 8 tokens: sums, and marks of NaN scales
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nt][r] += __shfl_xor_sync(kFull, l[nt][r], d);
+        if constexpr (FMT == RR_E2M1) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) broken |= __shfl_xor_sync(kFull, broken, d);
+            if (broken) {
+                const int grp = DH == 128 ? g / 2 : g / 4;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (broken >> ((nt * 2 + r) * W::kGroups + grp) & 1)
+#pragma unroll
+                            for (int i = 0; i < kMT; ++i) o[i][nt][r] = o[i][nt][2 + r] = NAN;
+            }
+        }
+
+        // The warps' results, joined through the ring's memory: every warp leaves
+        // its state, and takes (tile of dims, tile of rows) pairs to join.
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+#if __CUDA_ARCH__ >= 900
+        cudaTriggerProgrammaticLaunchCompletion();
+#endif
+        {
+            float *at = s_merge + warp * 32 * kKeep + lane;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int r = c & 1;
-                    // -inf - -inf: a row that has seen nothing yet
-                    const bool none = s[u][nt][c] == -INFINITY;
-                    const float x = s[u][nt][c] - m1[nt][r];
-                    l[nt][r] += none ? 0.f : ex2(x);
-                    w[c] = none ? 0.f : ex2(x + (ev[u][c >> 1] - m2[nt][r] + kLift));
-                }
-                pb[nt][0] = transpose_8x8(pack_f16(w[0], w[1]));
-                pb[nt][1] = transpose_8x8(pack_f16(w[2], w[3]));
-            }
-
-            // O^T: dims (DH / 8) g + 2 i (rows g) and + 1 (rows g + 8) of tile i
-            uint32_t v[4][W::kV];
+                for (int i = 0; i < kMT; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) read_value<FMT, DH>(v[q], st, 2 * t + (q & 1) + 8 * (q >> 1), g);
+                    for (int c = 0; c < 4; ++c) at[32 * ((nt * kMT + i) * 4 + c)] = o[i][nt][c];
 #pragma unroll
-            for (int j = 0; j < W::kV; ++j) {
-                if constexpr (FMT == RR_E4M3) {
-                    const uint32_t x0 = __byte_perm(v[0][j], v[1][j], 0x5140), x1 = __byte_perm(v[2][j], v[3][j], 0x5140);
-                    const uint32_t y0 = __byte_perm(v[0][j], v[1][j], 0x7362), y1 = __byte_perm(v[2][j], v[3][j], 0x7362);
-                    const uint32_t a[4] = {f16x2_of_e4m3(x0), f16x2_of_e4m3(x0 >> 16), f16x2_of_e4m3(x1),
-                                           f16x2_of_e4m3(x1 >> 16)};
-                    const uint32_t c[4] = {f16x2_of_e4m3(y0), f16x2_of_e4m3(y0 >> 16), f16x2_of_e4m3(y1),
-                                           f16x2_of_e4m3(y1 >> 16)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(o[2 * j][nt], a, pb[nt][0], pb[nt][1]);
-                        mma_f16(o[2 * j + 1][nt], c, pb[nt][0], pb[nt][1]);
-                    }
-                } else {
-                    // byte i of a row holds dims 2i (low half) and 2i + 1
-                    const uint32_t lo0 = (v[0][j] & 0x0f0f0f0fu) | (v[1][j] & 0x0f0f0f0fu) << 4;
-                    const uint32_t hi0 = ((v[0][j] >> 4) & 0x0f0f0f0fu) | (v[1][j] & 0xf0f0f0f0u);
-                    const uint32_t lo1 = (v[2][j] & 0x0f0f0f0fu) | (v[3][j] & 0x0f0f0f0fu) << 4;
-                    const uint32_t hi1 = ((v[2][j] >> 4) & 0x0f0f0f0fu) | (v[3][j] & 0xf0f0f0f0u);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t a[4] = {mul_f16x2(f16x2_of_e2m1(lo0 >> (8 * q)), vf[u][0]),
-                                               mul_f16x2(f16x2_of_e2m1(hi0 >> (8 * q)), vf[u][0]),
-                                               mul_f16x2(f16x2_of_e2m1(lo1 >> (8 * q)), vf[u][1]),
-                                               mul_f16x2(f16x2_of_e2m1(hi1 >> (8 * q)), vf[u][1])};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * j + q][nt], a, pb[nt][0], pb[nt][1]);
-                    }
+                for (int r = 0; r < 2; ++r) {
+                    float *st = at + 32 * (NT * kMT * 4 + nt * 6 + 3 * r);
+                    st[0] = m1[nt][r];
+                    st[32] = m2[nt][r];
+                    st[64] = l[nt][r];
                 }
             }
         }
-    }
-
-    // the lanes of a row's 8 tokens: sums, and marks of NaN scales
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[nt][r] += __shfl_xor_sync(kFull, l[nt][r], d);
-    if constexpr (FMT == RR_E2M1) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) broken |= __shfl_xor_sync(kFull, broken, d);
-        if (broken) {
-            const int grp = DH == 128 ? g / 2 : g / 4;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    if (broken >> ((nt * 2 + r) * W::kGroups + grp) & 1)
-#pragma unroll
-                        for (int i = 0; i < kMT; ++i) o[i][nt][r] = o[i][nt][2 + r] = NAN;
-        }
-    }
-
-    // The warps' results, joined through the ring's memory: every warp leaves
-    // its state, and takes (tile of dims, tile of rows) pairs to join.
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-#if __CUDA_ARCH__ >= 900
-    cudaTriggerProgrammaticLaunchCompletion();
-#endif
-    {
-        float *at = s_merge + warp * 32 * kKeep + lane;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < kMT; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) at[32 * ((nt * kMT + i) * 4 + c)] = o[i][nt][c];
+        __syncthreads();
+        for (int pair = warp; pair < kMT * NT; pair += kAttnWarps) {
+            const int nt = pair / kMT, i = pair % kMT;
+            const float *at = s_merge + lane;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float *st = at + 32 * (NT * kMT * 4 + nt * 6 + 3 * r);
-                st[0] = m1[nt][r];
-                st[32] = m2[nt][r];
-                st[64] = l[nt][r];
+                const int row = row0 + nt * 8 + 2 * t + r;
+                if (row >= p.rows) continue;
+                const float *st = at + 32 * (NT * kMT * 4 + nt * 6 + 3 * r), *os = at + 32 * (pair * 4 + r);
+                float a[kAttnWarps], c[kAttnWarps], n1 = -INFINITY, n2 = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    a[w] = st[w * 32 * kKeep];
+                    n1 = fmaxf(n1, a[w]);
+                }
+                const float b1 = n1 == -INFINITY ? 0.f : n1;
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    a[w] -= b1;
+                    c[w] = st[w * 32 * kKeep + 32] + a[w];
+                    n2 = fmaxf(n2, c[w]);
+                }
+                const float b2 = n2 == -INFINITY ? 0.f : n2;
+                float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    const float f = ex2(c[w] - b2);
+                    sum += st[w * 32 * kKeep + 64] * ex2(a[w]);
+                    x += os[w * 32 * kKeep] * f;
+                    y += os[w * 32 * kKeep + 64] * f;
+                }
+                const int dim = (DH / 8) * g + 2 * i;
+                const int back = p.n.q_tokens - 1 - row / p.group, near = max(0, *s_near - back);
+                if (p.mode != kOne) {
+                    // a part's number is share + job: both grow, one at a time; with splits
+                    // job * blocks + split
+                    float *part = (p.mode == kCluster ? s_part : p.part + (size_t)(blockIdx.x + job) * kRows * (DH + kState)) +
+                                  (row - row0) * (DH + kState);
+                    *reinterpret_cast<float2 *>(part + dim) = make_float2(x, y);
+                    if (g == 0 && i == 0) *reinterpret_cast<float4 *>(part + DH) = make_float4(n1, sum, n2, (float)near);
+                } else {
+                    write_out<DH>(p, b, head, row, dim, x, y, n1, sum, n2, (float)near);
+                }
             }
         }
-    }
-    __syncthreads();
-    for (int pair = warp; pair < kMT * NT; pair += kAttnWarps) {
-        const int nt = pair / kMT, i = pair % kMT;
-        const float *at = s_merge + lane;
+        if (p.mode == kShares) {
+            cur += end - begin;
+            if (cur >= stop) return;
+            __syncthreads();      // the block is done with this job's queries and sums
+            continue;
+        }
+        if (p.mode != kCluster) return;
+        // The blocks that share these tokens are a cluster: each joins a part of the
+        // results out of all blocks' shared memory.
+        cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        const int valid = min(kRows, p.rows - row0);
+        for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < valid * (DH / 2); i += gridDim.x * blockDim.x) {
+            const int r = i / (DH / 2), dim = i % (DH / 2) * 2;
+            float n1 = -INFINITY, n2 = -INFINITY, near = 0.f;
+            float4 st[kMaxCluster];
+            float2 xy[kMaxCluster];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = row0 + nt * 8 + 2 * t + r;
-            if (row >= p.rows) continue;
-            const float *st = at + 32 * (NT * kMT * 4 + nt * 6 + 3 * r), *os = at + 32 * (pair * 4 + r);
-            float a[kAttnWarps], c[kAttnWarps], n1 = -INFINITY, n2 = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                a[w] = st[w * 32 * kKeep];
-                n1 = fmaxf(n1, a[w]);
+            for (int s = 0; s < kMaxCluster; ++s) {
+                if (s < p.blocks) {
+                    const float *at = cluster.map_shared_rank(s_part, s) + r * (DH + kState);
+                    st[s] = *reinterpret_cast<const float4 *>(at + DH);
+                    xy[s] = *reinterpret_cast<const float2 *>(at + dim);
+                    n1 = fmaxf(n1, st[s].x);
+                    near = st[s].w;
+                }
             }
             const float b1 = n1 == -INFINITY ? 0.f : n1;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                a[w] -= b1;
-                c[w] = st[w * 32 * kKeep + 32] + a[w];
-                n2 = fmaxf(n2, c[w]);
+            for (int s = 0; s < kMaxCluster; ++s) {
+                if (s < p.blocks) {
+                    st[s].x -= b1;
+                    st[s].z += st[s].x;
+                    n2 = fmaxf(n2, st[s].z);
+                }
             }
             const float b2 = n2 == -INFINITY ? 0.f : n2;
             float sum = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = ex2(c[w] - b2);
-                sum += st[w * 32 * kKeep + 64] * ex2(a[w]);
-                x += os[w * 32 * kKeep] * f;
-                y += os[w * 32 * kKeep + 64] * f;
+            for (int s = 0; s < kMaxCluster; ++s) {
+                if (s < p.blocks) {
+                    const float f = ex2(st[s].z - b2);
+                    sum += st[s].y * ex2(st[s].x);
+                    x += xy[s].x * f;
+                    y += xy[s].y * f;
+                }
             }
-            const int dim = (DH / 8) * g + 2 * i;
-            const int back = p.n.q_tokens - 1 - row / p.group, near = max(0, *s_near - back);
-            if (p.splits > 1) {
-                float *part = p.cluster
-                                  ? s_part + (row - row0) * (DH + kState)
-                                  : p.part + (((size_t)blockIdx.y * p.splits + blockIdx.x) * p.rows + row) * (DH + kState);
-                *reinterpret_cast<float2 *>(part + dim) = make_float2(x, y);
-                if (g == 0 && i == 0) *reinterpret_cast<float4 *>(part + DH) = make_float4(n1, sum, n2, (float)near);
-            } else {
-                write_out<DH>(p, b, head, row, dim, x, y, n1, sum, n2, (float)near);
-            }
+            write_out<DH>(p, b, head, row0 + r, dim, x, y, n1, sum, n2, near);
         }
+        cluster.sync();      // no block leaves while its memory is read
+        return;
     }
-    if (!p.cluster) return;
-    // The blocks that share these tokens are a cluster: each joins a part of the
-    // results out of all blocks' shared memory.
-    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-    cluster.sync();
-    const int valid = min(kRows, p.rows - row0);
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < valid * (DH / 2); i += p.splits * blockDim.x) {
-        const int r = i / (DH / 2), dim = i % (DH / 2) * 2;
-        float n1 = -INFINITY, n2 = -INFINITY, near = 0.f;
-        float4 st[kMaxCluster];
-        float2 xy[kMaxCluster];
-#pragma unroll
-        for (int s = 0; s < kMaxCluster; ++s) {
-            if (s < p.splits) {
-                const float *at = cluster.map_shared_rank(s_part, s) + r * (DH + kState);
-                st[s] = *reinterpret_cast<const float4 *>(at + DH);
-                xy[s] = *reinterpret_cast<const float2 *>(at + dim);
-                n1 = fmaxf(n1, st[s].x);
-                near = st[s].w;
-            }
-        }
-        const float b1 = n1 == -INFINITY ? 0.f : n1;
-#pragma unroll
-        for (int s = 0; s < kMaxCluster; ++s) {
-            if (s < p.splits) {
-                st[s].x -= b1;
-                st[s].z += st[s].x;
-                n2 = fmaxf(n2, st[s].z);
-            }
-        }
-        const float b2 = n2 == -INFINITY ? 0.f : n2;
-        float sum = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-        for (int s = 0; s < kMaxCluster; ++s) {
-            if (s < p.splits) {
-                const float f = ex2(st[s].z - b2);
-                sum += st[s].y * ex2(st[s].x);
-                x += xy[s].x * f;
-                y += xy[s].y * f;
-            }
-        }
-        write_out<DH>(p, b, head, row0 + r, dim, x, y, n1, sum, n2, near);
-    }
-    cluster.sync();      // no block leaves while its memory is read
 }
 
-// Joins the splits of one row: a block per row, its warps take splits in turn,
-// a lane DH / 32 dims.  Launched while the attention's last blocks still run
-// (its results are waited for below), which hides the launch.
-template <int DH>
+// Joins the parts of one row: a block per row, its warps take parts in turn, a lane
+// DH / 32 dims.  Launched while the attention's last blocks still run (its results
+// are waited for below), which hides the launch.
+template <int DH, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __grid_constant__ Cached p) {
-    constexpr int E = DH / 32;
+    constexpr int E = DH / 32, kRows = 8 * NT;
     __shared__ float s_o[kJoinWarps][DH], s_l[kJoinWarps];
+    __shared__ int s_prefix[kMaxShared + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.x / p.rows, row = blockIdx.x % p.rows, head = bh % p.c.heads, b = bh / p.c.heads;
-    const float *at = p.part + ((size_t)bh * p.splits * p.rows + row) * (DH + kState);
-    const size_t stride = (size_t)p.rows * (DH + kState);
+    const int hz = p.c.heads * p.zs, in_b = head * p.zs + row / kRows;
+    int parts = p.blocks;
+    size_t part = (size_t)(b * hz + in_b) * p.blocks;      // its first
+    if (p.mode == kShares) {
+        sum_steps(p, s_prefix);
+        const int steps = s_prefix[b + 1] - s_prefix[b];
+        const long long total = (long long)s_prefix[p.n.batch] * hz, first = (long long)s_prefix[b] * hz + (long long)in_b * steps;
+        // the shares that the job's first and last step are in
+        const int c0 = steps ? (int)(((first + 1) * p.blocks - 1) / total) : 0;
+        parts = steps ? (int)(((first + steps) * p.blocks - 1) / total) - c0 + 1 : 0;
+        part = (size_t)c0 + b * hz + in_b;
+    }
+    const float *at = p.part + (part * kRows + row % kRows) * (DH + kState);
+    const size_t stride = (size_t)kRows * (DH + kState);
 #if __CUDA_ARCH__ >= 900
     cudaGridDependencySynchronize();
 #endif
     float n1 = -INFINITY, n2 = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) n1 = fmaxf(n1, at[s * stride + DH]);
+    for (int s = lane; s < parts; s += 32) n1 = fmaxf(n1, at[s * stride + DH]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
     const float b1 = n1 == -INFINITY ? 0.f : n1;
-    for (int s = lane; s < p.splits; s += 32) n2 = fmaxf(n2, at[s * stride + DH + 2] + (at[s * stride + DH] - b1));
+    for (int s = lane; s < parts; s += 32) n2 = fmaxf(n2, at[s * stride + DH + 2] + (at[s * stride + DH] - b1));
 #pragma unroll
     for (int d = 16; d; d >>= 1) n2 = fmaxf(n2, __shfl_xor_sync(kFull, n2, d));
     const float b2 = n2 == -INFINITY ? 0.f : n2;
@@ -865,7 +970,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __gr
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int s = warp; s < p.splits; s += kJoinWarps) {
+    for (int s = warp; s < parts; s += kJoinWarps) {
         const float *x = at + s * stride;
         const float4 st = *reinterpret_cast<const float4 *>(x + DH);
         float v[E];
@@ -890,7 +995,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __gr
         x += s_o[w][d];
         y += s_o[w][d + 1];
     }
-    write_out<DH>(p, b, head, row, d, x, y, n1, l, n2, at[DH + 3]);
+    write_out<DH>(p, b, head, row, d, x, y, n1, l, n2, parts ? at[DH + 3] : 0.f);
 }
 
 bool config_ok(const rr_cache_config *c, const rr_cached_attn_config *n) {
@@ -920,75 +1025,83 @@ int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
     return c->dh == 64 || (twos % 2 == 0 && (long long)n->batch * c->heads * twos > 148) ? 4 : 2;
 }
 
-// CTAs that share a sequence's tokens, and how their results are joined.  A CTA
-// costs its share of the steps and a start and an end worth about 24 of them;
-// CTAs come in waves of 148 SMs, of which the last is half empty when there is
-// more than one.  Measured: 16 sequences of 512 steps and 8 heads, 2 CTAs each
-// (256 in one wave) 72 us, 3 (two waves) 88 us; 64 sequences of up to 751 steps,
-// 1 CTA each 250 us, 2 216 us, 3 223 us.  No CTA gets less than a pair of steps
-// for each warp.  Joining through the workspace takes a second launch, for
-// caller and GPU together about 36 steps; a cluster needs none, but clusters do
-// not pack (24 sequences of 188 steps and 2 heads, 3 CTAs each in clusters 43 us,
-// joined through the workspace 26 us), so they are for at most half the SMs (one
-// sequence of 256 steps and 8 heads: 11.3 us and 18.7 with the caller's share, 12.7
-// and 28 through the workspace).
-struct Splits {
-    int n;
-    bool cluster;
+// The cut of a call (above) with the least cost, in steps.  A job costs its steps and
+// a start and an end worth about 24; CTAs come in waves of 148 SMs.  Sequences are
+// taken to have three quarters of the table's length on average, and all of a
+// route's.  Parts in the workspace take a second launch, for caller and GPU together
+// about 36 steps, and shares, which are even whatever the lengths, 12 more for every
+// CTA to find its own.  A cluster needs no second launch, but clusters do not pack,
+// so they are for at most half the SMs.  Measured, with 8 heads and up to 751 steps:
+// 24 sequences by splits 105 us, by shares 91; 64 sequences 217 and 222; with 2 heads
+// and 188 steps, 24 sequences in clusters of 3 43 us, by 3 splits 26, by shares 32;
+// with 8 heads and 256 steps, one sequence in a cluster 11.3 us and 18.7 with the
+// caller's share, by splits 12.7 and 28.
+struct Cut {
+    int mode, blocks, zs;
 };
-Splits splits_of(const rr_cache_config *c, const rr_cached_attn_config *n, bool route) {
+Cut cut_of(const rr_cache_config *c, const rr_cached_attn_config *n, bool route) {
     const long long rows = (long long)(n->q_heads / c->heads) * n->q_tokens;
     const int nt = tiles_of(c, n), slots = 148 * ctas_per_sm(c->dh, nt);
-    const long long blocks = (long long)n->batch * c->heads * ((rows + 8 * nt - 1) / (8 * nt));
-    const long long steps = (long long)(route ? n->width : n->table_width) * (c->chunk / 16);
-    if (blocks == 0) return {1, false};
-    const long long most = steps / (2 * kAttnWarps), tried = 4 * slots / blocks + 1;
-    Splits best = {1, false};
+    const int zs = (int)((rows + 8 * nt - 1) / (8 * nt));
+    const long long jobs = (long long)n->batch * c->heads * zs;
+    const double steps = (double)(route ? n->width : n->table_width) * (c->chunk / 16), fill = route ? 1.0 : 0.75;
+    Cut best = {kOne, 1, zs};
+    if (jobs == 0) return best;
     double least = 1e300;
-    for (int s = 1; s == 1 || (s <= most && s <= tried); ++s) {
-        const bool cluster = s > 1 && s <= kMaxCluster && blocks * s <= 74;
-        const double ctas = (double)blocks * s, waves = ctas <= slots ? 1.0 : ctas / slots + 0.5;
-        const double cost = waves * ((double)steps / s + 24.0) + (s > 1 && !cluster ? 36.0 : 0.0);
-        if (cost < least) least = cost, best = {s, cluster};
+    const long long tried = 4 * slots / jobs + 1;
+    for (int s = 1; s == 1 || (s <= tried && steps / s >= 2 * kAttnWarps); ++s) {
+        const double one = steps / s + 24.0, waves = (double)jobs * s / slots;
+        double cost = waves <= 1.0 ? one : ((fill * waves > 1.0 ? fill * waves : 1.0) + 0.4) * one;
+        int mode = s == 1 ? kOne : kCluster;
+        if (s > kMaxCluster || (s > 1 && jobs * s > 74)) mode = kSplits, cost += 36.0;
+        if (cost < least) least = cost, best = {mode, s, zs};
     }
+    // (sums of steps are int)
+    const double work = fill * jobs * steps;
+    const int shares = work / (2 * kAttnWarps) < slots ? (int)(work / (2 * kAttnWarps)) : slots;
+    if (n->batch <= kMaxShared && n->batch * steps < 1e9 && shares > 1 &&
+        work / shares + 24.0 * (1.0 + (double)jobs / shares) + 48.0 < least)
+        best = {kShares, shares, zs};
     return best;
+}
+
+size_t part_bytes(const rr_cache_config *c, const rr_cached_attn_config *n, const Cut &cut) {
+    const size_t jobs = (size_t)n->batch * c->heads * cut.zs;
+    const size_t parts = cut.mode == kSplits ? jobs * cut.blocks : cut.mode == kShares ? jobs + cut.blocks : 0;
+    return parts * 8 * tiles_of(c, n) * (c->dh + kState) * sizeof(float);
 }
 
 template <int FMT, int DH, int NT>
 cudaError_t launch(const Cached &p, cudaStream_t s) {
-    const int smem = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 + joined_bytes<FMT, DH, NT>() + 8 * NT * (DH + kState) * 4;
+    const int most = 8 * NT * (DH + 4) * 2 + 8 * NT * 4 + 16 + joined_bytes<FMT, DH, NT>() + 8 * NT * (DH + kState) * 4 +
+                     4 * (kMaxShared + 1);
+    const int smem = most - (p.mode == kShares ? 4 * (kMaxShared - p.n.batch) : 4 * (kMaxShared + 1));
     auto kern = cached_attention_kernel<FMT, DH, NT>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), smem, done);
+    cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), most, done);
     if (e != cudaSuccess) return e;
-    const dim3 grid(p.splits, p.n.batch * p.c.heads, (p.rows + 8 * NT - 1) / (8 * NT));
-    if (p.cluster) {
-        cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t config = {};
+    config.blockDim = dim3(32 * kAttnWarps);
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    config.attrs = &attr;
+    config.gridDim = p.mode == kShares ? dim3(p.blocks) : dim3(p.blocks, p.n.batch * p.c.heads, p.zs);
+    if (p.mode == kCluster) {
         attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = p.splits;
+        attr.val.clusterDim.x = p.blocks;
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t config = {};
-        config.gridDim = grid;
-        config.blockDim = dim3(32 * kAttnWarps);
-        config.dynamicSmemBytes = smem;
-        config.stream = s;
-        config.attrs = &attr;
         config.numAttrs = 1;
-        return cudaLaunchKernelEx(&config, kern, p);
     }
-    kern<<<grid, 32 * kAttnWarps, smem, s>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t join = {};
-    join.gridDim = dim3((unsigned)p.n.batch * p.c.heads * p.rows);
-    join.blockDim = dim3(32 * kJoinWarps);
-    join.stream = s;
-    join.attrs = &early;
-    join.numAttrs = 1;
-    return cudaLaunchKernelEx(&join, cached_join_kernel<DH>, p);
+    e = cudaLaunchKernelEx(&config, kern, p);
+    if (e != cudaSuccess || p.mode < kSplits) return e;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    config.numAttrs = 1;
+    config.gridDim = dim3((unsigned)p.n.batch * p.c.heads * p.rows);
+    config.blockDim = dim3(32 * kJoinWarps);
+    config.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&config, cached_join_kernel<DH, NT>, p);
 }
 
 template <int FMT, int DH>
@@ -1006,9 +1119,7 @@ extern "C" size_t rr_cached_attention_workspace_bytes(const rr_cache_config *cfg
                                                       int32_t routed) {
     using namespace rr_cache;
     if (!config_ok(cfg, attn)) return 0;
-    const Splits splits = splits_of(cfg, attn, routed != 0);
-    if (splits.n == 1 || splits.cluster) return 0;
-    return (size_t)attn->batch * attn->q_heads * attn->q_tokens * splits.n * (cfg->dh + kState) * sizeof(float);
+    return part_bytes(cfg, attn, cut_of(cfg, attn, routed != 0));
 }
 
 extern "C" rr_status rr_cached_attention(const rr_cache_config *cfg, const rr_cache_pool *pool,
@@ -1024,7 +1135,8 @@ extern "C" rr_status rr_cached_attention(const rr_cache_config *cfg, const rr_ca
     if (!a.seq_lens || !aligned(a.seq_lens, 4) || !aligned(a.route, 4) || !aligned(a.slopes, 4) || !aligned(a.lse, 4))
         return RR_EINVAL;
     if (attn->table_width > 0 && (!a.page_table || !aligned(a.page_table, 4))) return RR_EINVAL;
-    const size_t need = rr_cached_attention_workspace_bytes(cfg, attn, a.route != nullptr);
+    const Cut cut = cut_of(cfg, attn, a.route != nullptr);
+    const size_t need = part_bytes(cfg, attn, cut);
     if (need > 0 && (!workspace || !aligned(workspace, 256))) return RR_EINVAL;
     if (workspace_bytes < need) return RR_ENOMEM;
     Cached p;
@@ -1036,9 +1148,9 @@ extern "C" rr_status rr_cached_attention(const rr_cache_config *cfg, const rr_ca
     p.shift = chunk_shift(cfg->chunk);
     p.group = attn->q_heads / cfg->heads;
     p.rows = p.group * attn->q_tokens;
-    const Splits splits = splits_of(cfg, attn, a.route != nullptr);
-    p.splits = splits.n;
-    p.cluster = splits.cluster;
+    p.mode = cut.mode;
+    p.blocks = cut.blocks;
+    p.zs = cut.zs;
     const float scale = attn->scale > 0.f ? attn->scale : 1.0f / sqrtf((float)cfg->dh);
     p.s1 = attn->soft_cap > 0.f ? scale / attn->soft_cap : scale * kLog2e;
     p.s2 = attn->soft_cap * kLog2e;

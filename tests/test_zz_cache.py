@@ -283,6 +283,25 @@ def test_attention_matches_the_oracle(rr, case, kind):
     check(got, codes, scales, fmt, q, lens, table, route, **kw)
 
 
+@pytest.mark.parametrize("fmt,dh,chunk,heads,group,qt,batch,most", [
+    ("e4m3", 64, 64, 4, 2, 1, 40, 3000),      # shares that end inside jobs and hold several
+    ("e2m1", 128, 16, 2, 4, 1, 60, 900),
+    ("e4m3", 64, 32, 1, 8, 5, 30, 1500),      # ... of two row blocks
+    ("e4m3", 64, 16, 2, 8, 4, 24, 3001),      # three blocks to each job
+    ("e2m1", 64, 128, 1, 2, 1, 3, 9000)])
+def test_ragged_batches(rr, fmt, dh, chunk, heads, group, qt, batch, most):
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.integers(most // 3, most, batch)]
+    lens[0], lens[1], lens[-1] = most, 0, 1
+    if batch > 5:
+        lens[3:5] = [0, 0]
+    case = cached_case(lens=lens, fmt=fmt, dh=dh, chunk=chunk, heads=heads, group=group, qt=qt, seed=batch)
+    slopes = torch.tensor([2.0 ** -(h + 1) for h in range(heads * group)]).to(DEV)
+    for kw in (dict(), dict(slopes=slopes)):
+        got = rr.cached_attention(*case[:2], case[3], _i32(case[4]), _i32(case[5]), return_lse=True, **kw)
+        check(got, *case, **kw)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_scales_that_differ_by_many_binades(rr, fmt):
     case = cached_case(lens=[300, 90], fmt=fmt, dh=128, spread=24, q_scale=2.0 ** -24, group=4)
