@@ -191,50 +191,75 @@ __device__ __forceinline__ int nearest(const Masked &p, const Unit &u, const int
     return best;
 }
 
-// One row computed by a warp, key by key, reading only what it sees: the way
-// out for a row whose accumulators hold an infinity or a NaN.  There a masked
-// value row that holds one has met a weight of zero in the matrix product, or
-// the row's own result is not finite; both end here with the right values.
+// One row computed by a warp on the CUDA cores, reading only what it sees: the way
+// out for a row whose accumulators hold an infinity or a NaN.  There a masked value
+// row that holds one has met a weight of zero in the matrix product, or the row's
+// own result is not finite; both end here with the right values.  32 keys at a time:
+// a lane scores one, then the warp adds their values, a lane DH / 32 dims (about 100
+// cycles a key; waits for a block with such rows stay far below their bound).
 // `row` numbers the unit's rows.
 template <typename T, int DH>
-__device__ __noinline__ void row_alone(const Masked &p, const Unit &u, const int32_t *list, int n, int row, int near) {
+__device__ __forceinline__ void row_alone(const Masked &p, const Unit &u, const int32_t *list, int n, int row, int near) {
     constexpr int E = DH / 32;
     const int lane = threadIdx.x & 31;
     const int head = u.route_head * p.group + (row >> p.shift), token = (u.i << p.shift) + (row & (p.c.chunk - 1));
     const int pos = p.c.q_offset + token;
-    const T *q = static_cast<const T *>(p.a.q) + u.b * p.c.q_stride[0] + head * p.c.q_stride[1] +
-                 token * p.c.q_stride[2] + lane * E;
-    const T *k = static_cast<const T *>(p.a.k) + u.b * p.c.k_stride[0] + u.kv_head * p.c.k_stride[1] + lane * E;
+    const T *q = static_cast<const T *>(p.a.q) + u.b * p.c.q_stride[0] + head * p.c.q_stride[1] + token * p.c.q_stride[2];
+    const T *k = static_cast<const T *>(p.a.k) + u.b * p.c.k_stride[0] + u.kv_head * p.c.k_stride[1];
     const T *v = static_cast<const T *>(p.a.v) + u.b * p.c.v_stride[0] + u.kv_head * p.c.v_stride[1] + lane * E;
     const int doc = p.a.doc_q ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + token] : 0;
     const float slope = p.a.slopes ? p.a.slopes[head] * kLog2e : 0.f;
-    float qf[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        qf[e] = Half<T>::up(q[e]);
-        o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int it = 0; it < n; ++it) {
-        const int lo = (list[it] & kChunkId) << p.shift, hi = min(lo + p.c.chunk, p.c.nk_tokens);
-        for (int s = lo; s < hi; ++s) {
-            if (!in_sight(p, u.prefix, pos, s)) continue;
-            if (p.a.doc_q && (doc < 0 || p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] != doc)) continue;
-            float x = 0.f;
-            for (int e = 0; e < E; ++e) x += qf[e] * Half<T>::up(k[s * p.c.k_stride[2] + e]);
-            for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
+    float o[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 1
+    for (int slot0 = 0; slot0 < n << p.shift; slot0 += 32) {
+        const int slot = slot0 + lane;
+        const int s = slot < n << p.shift ? ((list[slot >> p.shift] & kChunkId) << p.shift) + (slot & (p.c.chunk - 1))
+                                          : INT_MAX;
+        bool see = s < p.c.nk_tokens && in_sight(p, u.prefix, pos, s);
+        if (see && p.a.doc_q) see = doc >= 0 && p.a.doc_k[(size_t)u.b * p.c.nk_tokens + s] == doc;
+        float x = -INFINITY;
+        if (see) {
+            x = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < DH; c += 8) {
+                const uint4 kw = *reinterpret_cast<const uint4 *>(k + s * p.c.k_stride[2] + c);
+                const uint4 qw = *reinterpret_cast<const uint4 *>(q + c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x += Half<T>::up(reinterpret_cast<const T *>(&qw)[e]) * Half<T>::up(reinterpret_cast<const T *>(&kw)[e]);
+            }
             x *= p.s1;
-            if (p.c.soft_cap > 0.f) x = p.s2 * tanhf(x);
+            if (p.c.soft_cap > 0.f) x = p.s2 * rr_attn::tanh_f32(x);
             if (p.a.slopes) x -= slope * (float)(abs(pos - s) - near);
-            const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.f : mn;
-            const float corr = exp2f(m - base), w = exp2f(x - base);
-            m = mn;
-            l = l * corr + w;
-            for (int e = 0; e < E; ++e)
-                o[e] = o[e] * corr + w * Half<T>::up(v[s * p.c.v_stride[2] + e]);
+        }
+        float top = x;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+        const float corr = rr_attn::ex2(m - base), w = rr_attn::ex2(x - base);
+        m = mn;
+        float sum = w;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+        l = l * corr + sum;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= corr;
+        unsigned seen = __ballot_sync(kFull, see);
+#pragma unroll 1
+        while (seen) {
+            const int from = __ffs(seen) - 1;
+            seen &= seen - 1;
+            const float wk = __shfl_sync(kFull, w, from);
+            const T *vk = v + __shfl_sync(kFull, s, from) * p.c.v_stride[2];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += wk * Half<T>::up(vk[e]);
         }
     }
     T *out = static_cast<T *>(p.a.out) + u.b * p.c.out_stride[0] + head * p.c.out_stride[1] +
              token * p.c.out_stride[2] + lane * E;
+#pragma unroll
     for (int e = 0; e < E; ++e) out[e] = Half<T>::down(l == 0.f ? 0.f : o[e] / l);
 }
 

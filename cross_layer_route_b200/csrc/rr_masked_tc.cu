@@ -259,19 +259,19 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 const int32_t *doc_k;
                 float slope;
                 {
-                const Unit u = unit_of(p, item);
-                const Row r0 = row_of(p, u);
-                pos = r0.pos;
-                doc = docs && r0.valid ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + r0.token] : -1;
-                doc_k = docs ? p.a.doc_k + (size_t)u.b * p.c.nk_tokens : nullptr;
-                // keys below this are in sight; none to a row without a document
-                limit = docs && doc < 0 ? 0 : min(p.c.nk_tokens, p.c.causal ? max(pos + 1, u.prefix) : p.c.nk_tokens);
-                slope = bias ? p.a.slopes[r0.head] * kLog2e : 0.f;
-                near = 0;
-                if (bias && ok) {
-                    near = nearest(p, u, list, n_list, pos, doc, 0, 1);
-                    if (near == INT_MAX) near = 0;
-                }
+                    const Unit u = unit_of(p, item);
+                    const Row r0 = row_of(p, u);
+                    pos = r0.pos;
+                    doc = docs && r0.valid ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + r0.token] : -1;
+                    doc_k = docs ? p.a.doc_k + (size_t)u.b * p.c.nk_tokens : nullptr;
+                    // keys below this are in sight; none to a row without a document
+                    limit = docs && doc < 0 ? 0 : min(p.c.nk_tokens, p.c.causal ? max(pos + 1, u.prefix) : p.c.nk_tokens);
+                    slope = bias ? p.a.slopes[r0.head] * kLog2e : 0.f;
+                    near = 0;
+                    if (bias && ok) {
+                        near = nearest(p, u, list, n_list, pos, doc, 0, 1);
+                        if (near == INT_MAX) near = 0;
+                    }
                 }
                 float m = -INFINITY, l = 0.f;
                 for (int j = 0; ok && j < n; ++j) {
@@ -634,8 +634,7 @@ bool tensor_map(const Masked &p, const void *base, int tokens, int heads, const 
     }
     const cuuint32_t box[4] = {64u, (cuuint32_t)box_tokens, 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
     return enc(map, p.c.dtype == RR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-               const_cast<void *>(base), dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B,
+               const_cast<void *>(base), dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
