@@ -466,6 +466,7 @@ bool config_ok(const rr_masked_attn_config *c) {
         if (out_sizes[i] > 1 && c->out_stride[i] == 0) return false;
     const long long group = c->q_heads / c->route_heads, chunks = (c->nq_tokens + c->chunk - 1) / c->chunk;
     const long long heads = (long long)c->batch * c->route_heads, rows16 = group * c->chunk / 16;
+    if (group * c->chunk > 1 << 24) return false;
     if (chunks > 0 && heads > 0x7fffffffLL / chunks) return false;
     if (heads * chunks > 0 && rows16 > 0x7fffffffLL / (heads * chunks)) return false;
     return true;

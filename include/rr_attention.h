@@ -94,9 +94,9 @@ rr_status rr_sparse_attention(const rr_attn_config *cfg, const void *d_q, const 
  * divides q_heads; dh in {64, 128}; chunk in {16, 32, 64, 128}; 0 <= width <=
  * 1024; route_stride >= max(width, 1); dtype RR_BF16 or RR_F16; q_offset >= 0
  * and q_offset + nq_tokens, nk_tokens <= 2^24 (positions are exact in fp32);
- * scale >= 0 and at most 1e30; soft_cap 0 or in [1e-3, 1e30]; batch * route_heads * query chunks *
- * ceil(q_heads / route_heads * chunk / 16) <= 2^31 - 1; strides in
- * elements, >= 0 and multiples of 8 (those of `out` of a size above 1, > 0). */
+ * scale >= 0 and at most 1e30; soft_cap 0 or in [1e-3, 1e30]; rows of a unit,
+ * q_heads / route_heads * chunk, <= 2^24, and 16ths of them times batch * route_heads *
+ * query chunks <= 2^31 - 1; strides in elements, >= 0 and multiples of 8 (those of `out` of a size above 1, > 0). */
 typedef struct {
     int32_t batch;
     int32_t q_heads;      /* query (and output) heads */
@@ -137,7 +137,7 @@ typedef struct {
  * rounded to the inputs' type for the product with v, and the result to that
  * type once.  Units of 128 and more rows (q_heads / route_heads * chunk) run on
  * tcgen05, smaller ones on mma.sync; both give the same bits from call to call.
- * Rows whose result is not finite take a slow path, key by key.  `out` must not
+ * Rows whose result is not finite take a slow path.  `out` must not
  * overlap the inputs.  Every wait inside the kernels is bounded (about a
  * second); should one run out, the rows not yet written become NaN.  Errors: RR_EINVAL (shape, stride, null or
  * misaligned pointer), RR_ECUDA (launch). */

@@ -44,6 +44,7 @@ def refused(call, *args, status=None):
     dict(soft_cap=1e-4), dict(soft_cap=math.inf), dict(soft_cap=math.nan), dict(q_stride=(51200, 6400, 60)),
     dict(k_stride=(-8, 6400, 64)), dict(v_stride=(1 << 41, 6400, 64)), dict(out_stride=(51200, 0, 64)),
     dict(batch=1 << 20, q_heads=1 << 16, kv_heads=1, route_heads=1 << 12),
+    dict(batch=1, nq_tokens=1, q_heads=1 << 27, kv_heads=1, route_heads=1, chunk=128),      # 2^34 rows to a unit
 ])
 def test_masked_attention_refuses_bad_shapes(bad):
     refused(rr.rr_masked_attention, masked_cfg(**bad), masked_args(), 0)
