@@ -46,7 +46,7 @@ __device__ __forceinline__ int count_le(const int32_t *cu, int n, int row) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = n;
     while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
+        const int step = (int)(((unsigned)(hi - lo) + 31u) / 32u);
         const long long at = lo + (long long)(lane + 1) * step - 1;
         const int c = __popc(__ballot_sync(0xffffffffu, at < hi && cu[at < hi ? at : lo] <= row));
         lo += c * step;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const __grid_c
     const int part = blockIdx.x % p.parts;
     const long long first = (long long)(blockIdx.x / p.parts) * p.tokens * kWarps + (threadIdx.x >> 5);
     if (first >= p.r.rows) return;
-    const int row0 = (int)first, tokens = min(p.tokens, (p.r.rows - row0 + kWarps - 1) / kWarps);
+    const int row0 = (int)first, tokens = min(p.tokens, (p.r.rows - row0 - 1) / kWarps + 1);
     const L l(part * kUnroll * L::kStep);
     const int64_t x_token = l.which ? p.v_stride[0] : p.k_stride[0];
     const int64_t x_step = (l.which ? p.v_stride[1] : p.k_stride[1]) * L::kStep;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_co
     const int part = blockIdx.x % p.parts;
     const long long first = (long long)(blockIdx.x / p.parts) * p.tokens * kWarps + (threadIdx.x >> 5);
     if (first >= p.r.rows) return;
-    const int row0 = (int)first, tokens = min(p.tokens, (p.r.rows - row0 + kWarps - 1) / kWarps);
+    const int row0 = (int)first, tokens = min(p.tokens, (p.r.rows - row0 - 1) / kWarps + 1);
     const L l(part * kUnroll * L::kStep);
     T *out = static_cast<T *>(l.which ? p.v : p.k);
     const int64_t x_token = l.which ? p.v_stride[0] : p.k_stride[0];
