@@ -527,7 +527,7 @@ def cache_empty(pages: int, heads: int, chunk: int, dh: int, fmt: str = "e4m3", 
     if rr_cache_scales_bytes(rr_cache_config(1, heads, dh, chunk, RR_E4M3)) == 0 or pages < 0:
         raise RRError(RR_EINVAL, f"cache_empty(pages={pages}, heads={heads}, chunk={chunk}, dh={dh})")
     row, groups = (dh, 1) if fmt == "e4m3" else (dh // 2, dh // 32)
-    mk = lambda n: torch.zeros((pages, heads, 2, chunk, n), dtype=torch.uint8, device=device or "cuda")
+    mk = lambda n: torch.zeros((pages, heads, 2, chunk, n), dtype=torch.uint8, device="cuda" if device is None else device)
     return mk(row), mk(groups)
 
 
@@ -772,6 +772,8 @@ class RouteLedger:
         """The ledger's ids in place, as [batch, route heads, query chunks, c]:
         its bh heads are `heads` route heads of each batch entry."""
         c = self.cfg
+        if chunk < 1:
+            raise ValueError(f"chunk: expected 1 or more, got {chunk}")
         if heads < 1 or c.bh % heads != 0:
             raise ValueError(f"route_heads: expected a divisor of the ledger's {c.bh} heads, got {heads}")
         if -(-nq_tokens // chunk) != c.nq or -(-nk_tokens // chunk) > c.nk:

@@ -2,6 +2,7 @@
 (include/rr_attention.h, include/rr_cache.h), and of their oracle against
 closed forms.  No GPU needed: refused calls return before any CUDA call."""
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -177,6 +178,21 @@ def test_bindings_refuse_host_tensors():
         rr.cache_empty(4, 2, 16, 64, fmt="int8")
     with pytest.raises(rr.RRError):
         rr.cache_empty(4, 2, 24, 64)
+
+
+def test_cache_empty_takes_any_name_of_a_device(monkeypatch):
+    named = []
+    monkeypatch.setattr(rr.torch, "zeros", lambda shape, dtype, device: named.append(device))
+    for device in (0, 1, "cuda:1", None):
+        rr.cache_empty(1, 1, 16, 64, device=device)
+    assert named == [0, 0, 1, 1, "cuda:1", "cuda:1", "cuda", "cuda"]
+
+
+def test_a_ledger_refuses_chunks_of_no_tokens():
+    ledger = SimpleNamespace(cfg=rr.Config(bh=2, nq=2, nk=2, d=64, k=2, m_near=0, r_rand=0))
+    for chunk in (0, -16):
+        with pytest.raises(ValueError):
+            rr.RouteLedger._route_of(ledger, 2, chunk, 32, 32)
 
 
 # ---- the oracle against closed forms ------------------------------------------------
