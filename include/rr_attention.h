@@ -125,7 +125,7 @@ typedef struct {
     const void *k;           /* [batch, kv_heads, nk_tokens, dh] by k_stride; 16-byte aligned */
     const void *v;           /* the same by v_stride */
     const int32_t *route;    /* [batch, route_heads, ceil(nq_tokens / chunk), route_stride] */
-    const float *slopes;     /* optional [q_heads]: bias by distance, finite and >= 0 */
+    const float *slopes;     /* optional [q_heads]: bias by distance, in [0, 1e30] */
     const int32_t *doc_q;    /* optional [batch, nq_tokens]: document of each query token */
     const int32_t *doc_k;    /* [batch, nk_tokens], given iff doc_q is */
     const int32_t *prefix;   /* optional [batch]: keys below it are visible under causal */

@@ -105,7 +105,9 @@ rr_status rr_cache_read(const rr_cache_config *cfg, const rr_cache_pool *pool, c
  * heads * q_tokens <= 256; batch * heads <= 65535; table_width * chunk <=
  * 2^24; 0 <= width <= 2^20, route_stride >= max(width, 1); scale >= 0 and at
  * most 1e30; soft_cap 0 or in [1e-3, 1e30]; dtype RR_BF16 or RR_F16; q strides >= 0,
- * multiples of 8. */
+ * multiples of 8.  A query row's largest magnitude times scale (with a cap, times
+ * scale / cap) is 0 or in [2^-112, 2^108], the keys' scales 2^e at most 2^100:
+ * outside of this, scores can lose bits or become infinite, which makes a row NaN. */
 typedef struct {
     int32_t batch;
     int32_t q_tokens;
@@ -125,7 +127,7 @@ typedef struct {
     const int32_t *seq_lens;    /* [batch] */
     const int32_t *page_table;  /* [batch, table_stride] */
     const int32_t *route;       /* optional [batch, heads, route_stride]; NULL: every chunk */
-    const float *slopes;        /* optional [q_heads], finite and >= 0 */
+    const float *slopes;        /* optional [q_heads], in [0, 1e30] */
     void *out;                  /* [batch, q_tokens, q_heads, dh], contiguous; 16-byte aligned */
     float *lse;                 /* optional [batch, q_tokens, q_heads] */
 } rr_cached_attn_args;

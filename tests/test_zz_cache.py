@@ -326,6 +326,19 @@ def test_extremes_of_the_queries(rr, fmt):
     assert (err <= np.where(fine, 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * mean + 1e-6, 1)).all()
 
 
+@pytest.mark.parametrize("power", [-96, 90])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_queries_and_keys_at_the_ends_of_their_range(rr, fmt, power):
+    # powers of two that cancel in the scores
+    codes, scales, fmt, q, lens, table = cached_case(lens=[48, 96], fmt=fmt, dh=64, group=4)
+    q *= 2.0 ** power
+    assert scales[:, :, 0].max() < 127 + 4 and scales[:, :, 0].min() > 90
+    scales[:, :, 0] -= power if power > 0 else 0
+    scales[:, :, 0] += -power if power < 0 else 0
+    got = rr.cached_attention(codes, scales, q, _i32(lens), _i32(table), return_lse=True)
+    check(got, codes, scales, fmt, q, lens, table)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_groups_that_hold_no_number(rr, fmt):
     # a NaN scale reaches the rows that see it, of its own dims for the values, and no others
