@@ -1018,11 +1018,14 @@ bool config_ok(const rr_cache_config *c, const rr_cached_attn_config *n) {
 // four of them fill the registers (one CTA per SM either way), so two are better
 // where four would stand half empty or few CTAs leave the SMs to latency: 16
 // sequences of up to 8000 tokens, 8 heads: 32 rows 148 us by fours and 165 by twos,
-// 40 rows 261 and 211; one such sequence, 32 rows: 39 and 30.
+// 40 rows 261 and 211; one such sequence, 32 rows: 39 and 30.  At dh 64 two CTAs of
+// twos fit an SM and one of fours, and the warps that hide latency are worth more than
+// the conversions: the same three by twos 73, 99 and 18.5 us, by fours 80, 137 and 21
+// (by ones 99, 120 and 20.5; three CTAs of twos spill: 109, 149 and 27).
 int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
     const int rows = n->q_heads / c->heads * n->q_tokens, twos = (rows + 15) / 16;
-    if (rows <= 16) return rows <= 8 ? 1 : 2;
-    return c->dh == 64 || (twos % 2 == 0 && (long long)n->batch * c->heads * twos > 148) ? 4 : 2;
+    if (rows <= 8) return 1;
+    return c->dh == 128 && twos % 2 == 0 && (long long)n->batch * c->heads * twos > 148 ? 4 : 2;
 }
 
 // The cut of a call (above) with the least cost, in steps.  A job costs its steps and
@@ -1108,9 +1111,10 @@ template <int FMT, int DH>
 cudaError_t launch_rows(const Cached &p, cudaStream_t s) {
     switch (tiles_of(&p.c, &p.n)) {
         case 1: return launch<FMT, DH, 1>(p, s);
-        case 2: return launch<FMT, DH, 2>(p, s);
+        case 4:
+            if constexpr (DH == 128) return launch<FMT, DH, 4>(p, s);
     }
-    return launch<FMT, DH, 4>(p, s);
+    return launch<FMT, DH, 2>(p, s);
 }
 
 }  // namespace rr_cache
