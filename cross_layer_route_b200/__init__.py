@@ -428,17 +428,12 @@ def _slopes(t, heads, index):
 
 
 def _rows_like(name, t, dtype, shape, index):
-    """Strides, all but the last, of a tensor of this type and shape whose rows
-    are contiguous; that of a size of one counts nothing."""
+    """Strides, all but the last, of a tensor of this type and shape whose rows are contiguous."""
     st = t.stride()
     if t.dtype is not dtype or t.shape != shape or st[-1] != 1 or t.get_device() != index:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{index}, the last dimension contiguous, "
                          f"got {_describe(t)}")
-    return _strides(st, shape) if 1 in shape else st[:-1]
-
-
-def _strides(strides, shape):
-    return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], strides))
+    return st[:-1]
 
 
 def masked_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, route: torch.Tensor, chunk: int,
@@ -489,8 +484,8 @@ def _masked_attention(handle, q, out, return_lse, ints, ptrs):
     shape = q.shape
     if out is None:
         out = torch.empty_like(q)
-    lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
-    status = _lib.rr_masked_attention(_MASKED_CFG.pack(*ints, *_strides(out.stride(), shape)),
+    lse = q.new_empty(tuple(shape[:3]), dtype=torch.float32) if return_lse else None
+    status = _lib.rr_masked_attention(_MASKED_CFG.pack(*ints, *out.stride()[:-1]),
                                       _MASKED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),
                                       handle)
     if status:
@@ -632,12 +627,12 @@ def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
 
 def _cached_attention(handle, q, out, return_lse, workspace, cfg, pool, attn, ptrs):
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = q.new_empty(tuple(q.shape[:3]), dtype=torch.float32) if return_lse else None
     if workspace is None:
         need = _lib.rr_cached_attention_workspace_bytes(cfg, attn, 1 if ptrs[3] else 0)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty((need,), dtype=torch.uint8)
     d_work, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _check(_lib.rr_cached_attention(cfg, pool, attn,
                                     _CACHED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),

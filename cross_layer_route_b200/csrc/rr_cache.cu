@@ -341,8 +341,9 @@ rr_status run(const rr_cache_config *cfg, const rr_cache_pool *pool, const rr_ca
         if (!stride[i] || !aligned(ptr[i], 16)) return RR_EINVAL;
         for (int j = 0; j < 2; ++j) {
             const int64_t x = stride[i][j];
+            if ((j == 0 ? rows->rows : cfg->heads) <= 1) continue;
             if (x < 0 || x > (1ll << 40) || x * size % 16 != 0) return RR_EINVAL;
-            if (!write && x < cfg->dh && (j == 0 ? rows->rows : cfg->heads) > 1) return RR_EINVAL;
+            if (!write && x < cfg->dh) return RR_EINVAL;
         }
     }
     if (rows->rows == 0 || rows->batch == 0 || (!k && !v)) return RR_OK;
@@ -357,8 +358,9 @@ rr_status run(const rr_cache_config *cfg, const rr_cache_pool *pool, const rr_ca
     p.k = k;
     p.v = v;
     for (int j = 0; j < 2; ++j) {
-        p.k_stride[j] = k ? k_stride[j] : 0;
-        p.v_stride[j] = v ? v_stride[j] : 0;
+        const bool counts = (j == 0 ? rows->rows : cfg->heads) > 1;
+        p.k_stride[j] = k && counts ? k_stride[j] : 0;
+        p.v_stride[j] = v && counts ? v_stride[j] : 0;
     }
     p.shift = chunk_shift(cfg->chunk);
     const int per_warp = (dtype == RR_F32 ? Eight<float>::kUnroll : Eight<__half>::kUnroll) * 128 / cfg->dh;   // heads

@@ -1009,8 +1009,11 @@ bool config_ok(const rr_cache_config *c, const rr_cached_attn_config *n) {
     if (n->width < 0 || n->route_stride < (n->width > 1 ? n->width : 1) || n->width > 1 << 20) return false;
     if (!(n->scale >= 0.f && n->scale <= 1e30f)) return false;
     if (n->soft_cap != 0.f && !(n->soft_cap >= 1e-3f && n->soft_cap <= 1e30f)) return false;
-    for (int64_t x : n->q_stride)
-        if (x < 0 || x % 8 != 0 || x > (1ll << 40)) return false;
+    const int sizes[3] = {n->batch, n->q_tokens, n->q_heads};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t x = n->q_stride[i];
+        if (sizes[i] > 1 && (x < 0 || x % 8 != 0 || x > (1ll << 40))) return false;
+    }
     return true;
 }
 
@@ -1036,7 +1039,7 @@ int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
 // CTA to find its own.  A cluster needs no second launch, but clusters do not pack,
 // so they are for at most half the SMs.  Measured, with 8 heads and up to 751 steps:
 // 24 sequences by splits 105 us, by shares 91; 64 sequences 217 and 222; with 2 heads
-// and 188 steps, 24 sequences in clusters of 3 43 us, by 3 splits 26, by shares 32;
+// and 188 steps, 24 sequences in clusters of 3 26.6 us, by 3 splits 22.5, by shares 27;
 // with 8 heads and 256 steps, one sequence in a cluster 11.3 us and 18.7 with the
 // caller's share, by splits 12.7 and 28.
 struct Cut {
@@ -1147,6 +1150,9 @@ extern "C" rr_status rr_cached_attention(const rr_cache_config *cfg, const rr_ca
     p.c = *cfg;
     p.pool = *pool;
     p.n = *attn;
+    if (attn->batch == 1) p.n.q_stride[0] = 0;
+    if (attn->q_tokens == 1) p.n.q_stride[1] = 0;
+    if (attn->q_heads == 1) p.n.q_stride[2] = 0;
     p.a = a;
     p.part = static_cast<float *>(workspace);
     p.shift = chunk_shift(cfg->chunk);

@@ -441,10 +441,17 @@ bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 
 bool soft_cap_ok(float x) { return x == 0.f || (x >= 1e-3f && x <= 1e30f); }
 
-bool strides_ok(const int64_t (&s)[3]) {
-    for (int64_t x : s)
-        if (x < 0 || x % 8 != 0 || x > (1ll << 40)) return false;
+// Strides of [batch, heads, tokens]; those of a size of one count nothing.
+bool strides_ok(const int64_t (&s)[3], int batch, int heads, int tokens) {
+    const int sizes[3] = {batch, heads, tokens};
+    for (int i = 0; i < 3; ++i)
+        if (sizes[i] > 1 && (s[i] < 0 || s[i] % 8 != 0 || s[i] > (1ll << 40))) return false;
     return true;
+}
+void drop_strides(int64_t (&s)[3], int batch, int heads, int tokens) {
+    if (batch <= 1) s[0] = 0;
+    if (heads <= 1) s[1] = 0;
+    if (tokens <= 1) s[2] = 0;
 }
 
 bool config_ok(const rr_masked_attn_config *c) {
@@ -459,7 +466,10 @@ bool config_ok(const rr_masked_attn_config *c) {
     if ((long long)c->q_offset + c->nq_tokens > 1 << 24 || c->nk_tokens > 1 << 24) return false;
     if (!(c->scale >= 0.f) || !isfinite(c->scale)) return false;
     if (!(c->scale <= 1e30f) || !soft_cap_ok(c->soft_cap)) return false;
-    if (!strides_ok(c->q_stride) || !strides_ok(c->k_stride) || !strides_ok(c->v_stride) || !strides_ok(c->out_stride))
+    if (!strides_ok(c->q_stride, c->batch, c->q_heads, c->nq_tokens) ||
+        !strides_ok(c->k_stride, c->batch, c->kv_heads, c->nk_tokens) ||
+        !strides_ok(c->v_stride, c->batch, c->kv_heads, c->nk_tokens) ||
+        !strides_ok(c->out_stride, c->batch, c->q_heads, c->nq_tokens))
         return false;
     const int out_sizes[3] = {c->batch, c->q_heads, c->nq_tokens};
     for (int i = 0; i < 3; ++i)
@@ -489,6 +499,10 @@ extern "C" rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const
         return RR_EINVAL;
     Masked p;
     p.c = *cfg;
+    drop_strides(p.c.q_stride, cfg->batch, cfg->q_heads, cfg->nq_tokens);
+    drop_strides(p.c.k_stride, cfg->batch, cfg->kv_heads, cfg->nk_tokens);
+    drop_strides(p.c.v_stride, cfg->batch, cfg->kv_heads, cfg->nk_tokens);
+    drop_strides(p.c.out_stride, cfg->batch, cfg->q_heads, cfg->nq_tokens);
     p.a = a;
     p.group = cfg->q_heads / cfg->route_heads;
     p.shift = cfg->chunk == 16 ? 4 : cfg->chunk == 32 ? 5 : cfg->chunk == 64 ? 6 : 7;

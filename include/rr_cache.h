@@ -76,8 +76,8 @@ typedef struct {
 } rr_cache_rows;
 
 /* Quantises and stores the rows of k and v (each [rows, heads, dh] of `dtype`:
- * RR_F32, RR_BF16 or RR_F16; strides of row and head in elements, rows 16-byte
- * aligned, dh contiguous).  Only places that a row falls on are written.
+ * RR_F32, RR_BF16 or RR_F16; strides of row and head in elements (of a size of one:
+ * any), rows 16-byte aligned, dh contiguous).  Only places that a row falls on are written.
  * Errors: RR_EINVAL, RR_ECUDA. */
 rr_status rr_cache_write(const rr_cache_config *cfg, const rr_cache_pool *pool, const rr_cache_rows *rows,
                          const void *d_k, const int64_t k_stride[2], const void *d_v,
@@ -105,7 +105,7 @@ rr_status rr_cache_read(const rr_cache_config *cfg, const rr_cache_pool *pool, c
  * heads * q_tokens <= 256; batch * heads <= 65535; table_width * chunk <=
  * 2^24; 0 <= width <= 2^20, route_stride >= max(width, 1); scale >= 0 and at
  * most 1e30; soft_cap 0 or in [1e-3, 1e30]; dtype RR_BF16 or RR_F16; q strides >= 0,
- * multiples of 8.  A query row's largest magnitude times scale (with a cap, times
+ * multiples of 8 (of a size of one: any).  A query row's largest magnitude times scale (with a cap, times
  * scale / cap) is 0 or in [2^-112, 2^108], the keys' scales 2^e at most 2^100:
  * outside of this, scores can lose bits or become infinite, which makes a row NaN. */
 typedef struct {

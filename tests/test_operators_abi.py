@@ -60,6 +60,22 @@ def test_masked_attention_refuses_bad_pointers(bad):
     refused(rr.rr_masked_attention, masked_cfg(), masked_args(**bad), 0)
 
 
+def test_strides_of_a_size_of_one_count_nothing():
+    # looked at before the pointers, so that a call that gets past them is refused for its null ones
+    odd = dict(q_stride=(-3, 7, 1), k_stride=(-3, 7, 1), v_stride=(-3, 7, 1), out_stride=(-3, 7, 1))
+    one = masked_cfg(batch=1, q_heads=1, kv_heads=1, route_heads=1, nq_tokens=0, nk_tokens=1, **odd)
+    rr.rr_masked_attention(one, masked_args(), 0)
+    one.nk_tokens = 2
+    refused(rr.rr_masked_attention, one, masked_args(), 0)
+    pool = rr.rr_cache_pool(P, P)
+    for call in (rr.rr_cache_write, rr.rr_cache_read):
+        call(cache(heads=1), pool, rows(rows=1, batch=0), P, (-3, 7), P, (1, 1), rr.RR_BF16, 0)
+        refused(call, cache(heads=1), pool, rows(rows=2, batch=0), P, (-3, 7), P, (64, 1), rr.RR_BF16, 0)
+    rr.rr_cached_attention(cache(heads=1), pool, attn(batch=1, q_heads=1, q_tokens=0, q_stride=(-3, 9, 1)), attn_args(), 0, 0, 0)
+    refused(rr.rr_cached_attention, cache(heads=1), pool, attn(batch=1, q_heads=2, q_tokens=0, q_stride=(-3, 9, 1)),
+            attn_args(), 0, 0, 0)
+
+
 def test_masked_attention_with_nothing_to_do():
     rr.rr_masked_attention(masked_cfg(batch=0), masked_args(), 0)
     rr.rr_masked_attention(masked_cfg(nq_tokens=0), masked_args(q=0, out=0), 0)

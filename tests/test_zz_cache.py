@@ -326,6 +326,22 @@ def test_extremes_of_the_queries(rr, fmt):
     assert (err <= np.where(fine, 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * mean + 1e-6, 1)).all()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_strides_of_a_size_of_one(rr, fmt):
+    g = torch.Generator().manual_seed(3)
+    k, v, q = (torch.randn(64, generator=g).to(BF).to(DEV) for _ in range(3))
+    codes, scales = rr.cache_empty(1, 1, 16, 64, fmt, DEV)
+    zero, cu, table = _i32([0]), _i32([0, 1]), _i32([[0]])
+    rr.cache_write(codes, scales, k.as_strided((1, 1, 64), (3, 5, 1)), v.as_strided((1, 1, 64), (1, 7, 1)), cu, zero, table)
+    got = tuple(torch.zeros(64, dtype=torch.float32, device=DEV) for _ in range(2))
+    rr.cache_read(codes, scales, cu, zero, table, 1, 64, torch.float32,
+                  out=tuple(x.as_strided((1, 1, 64), (2, 3, 1)) for x in got))
+    back = M.read_rows(codes.cpu().numpy(), scales.cpu().numpy(), fmt)[0, 0, :, 0]
+    assert np.array_equal(got[0].cpu().numpy(), back[0]) and np.array_equal(got[1].cpu().numpy(), back[1])
+    out = rr.cached_attention(codes, scales, q.as_strided((1, 1, 1, 64), (9, 3, 5, 1)), _i32([1]), table)
+    assert torch.equal(out.view(64), got[1].to(BF))      # one token's weight is one
+
+
 @pytest.mark.parametrize("power", [-96, 90])
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_queries_and_keys_at_the_ends_of_their_range(rr, fmt, power):

@@ -201,6 +201,16 @@ def test_strides_and_views(rr):
     assert (room[:, 0] == 7).all() and (room[:, nq + 1:] == 7).all() and (room[:, :, hq] == 7).all()
 
 
+@pytest.mark.parametrize("chunk,group", [(16, 1), (64, 8)])
+def test_strides_of_a_size_of_one(rr, chunk, group):
+    q, k, v, route = make(b=1, hq=group, hkv=1, nq=1, dh=64, chunk=chunk)
+    want = rr.masked_attention(q, k, v, route, chunk)
+    odd = [x.as_strided(x.shape, (3, 64 if x.shape[1] > 1 else 5, 7, 1)) for x in (q, k, v)]
+    out = torch.zeros(group, 64, dtype=q.dtype, device=DEV)
+    rr.masked_attention(*odd, route, chunk, out=out.as_strided((1, group, 1, 64), (9, 64, 11, 1)))
+    assert torch.equal(out, want.view(group, 64)) and out.any()
+
+
 @pytest.mark.parametrize("shape", [dict(chunk=16), dict(chunk=64, hq=8, hkv=2, dh=128)])
 def test_streams_and_graphs(rr, shape):
     q, k, v, route = make(seed=2, nq=150, **shape)
