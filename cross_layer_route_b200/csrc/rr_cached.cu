@@ -1040,8 +1040,8 @@ int tiles_of(const rr_cache_config *c, const rr_cached_attn_config *n) {
 // so they are for at most half the SMs.  Measured, with 8 heads and up to 751 steps:
 // 24 sequences by splits 105 us, by shares 91; 64 sequences 217 and 222; with 2 heads
 // and 188 steps, 24 sequences in clusters of 3 26.6 us, by 3 splits 22.5, by shares 27;
-// with 8 heads and 256 steps, one sequence in a cluster 11.3 us and 18.7 with the
-// caller's share, by splits 12.7 and 28.
+// with 8 heads and 256 steps, one sequence in a cluster 11.3 us and 15 with the
+// caller's share, by splits 12.7 and 20.
 struct Cut {
     int mode, blocks, zs;
 };
