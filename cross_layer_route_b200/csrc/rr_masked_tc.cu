@@ -69,7 +69,7 @@ struct TcShape {
     static constexpr int kStages = DH == 128 ? 4 : 8;
     static constexpr int kLists = 2 * (kMaxWidth + 4) * 4;        // lists and their lengths
     static constexpr int kBars = 2 * kStages + 4 * kTiles + 2 + 5;
-    static constexpr int kMisc = 64;
+    static constexpr int kMisc = 64 + kTileRows * 8;              // flags; the second group's states
     static constexpr int kSmem =
         1024 + kLists + kBars * 8 + kMisc + (kTiles + kStages) * kTileBytes;
 };
@@ -167,8 +167,8 @@ struct Row {
     int head, token, pos;
     bool valid;
 };
-__device__ __forceinline__ Row row_of(const Masked &p, const Unit &u) {
-    const int row = u.tile * kTiles * kTileRows + threadIdx.x, tok = row & (p.c.chunk - 1);
+__device__ __forceinline__ Row row_of(const Masked &p, const Unit &u, int thread) {
+    const int row = u.tile * kTiles * kTileRows + thread, tok = row & (p.c.chunk - 1);
     const bool in_unit = row < p.group << p.shift;
     Row r;
     r.head = u.route_head * p.group + (in_unit ? row >> p.shift : 0);
@@ -178,11 +178,23 @@ __device__ __forceinline__ Row row_of(const Masked &p, const Unit &u) {
     return r;
 }
 
+// The softmax warps' barrier.
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("bar.sync 2, %0;" ::"n"(32 * kSoftWarps) : "memory");
+}
+
+// SINGLE: units of one row tile.  Both softmax groups take it, the key tiles in turn,
+// with an S, an O, a maximum and a sum each, joined at the end: the tensor cores work
+// for one half of the keys while the other's softmax runs.  8192 tokens, 8 heads of 2
+// queries, chunks of 64, 32 routed: 159 -> 118 us at dh 64, 196 -> 146 at dh 128; with
+// a cap and a bias, chunks of 32 of 4 queries, 432 -> 317 and 479 -> 372; units of two
+// key tiles gain nothing and a unit of one loses 0.5 us.
+//
 // CAP and BIAS: whether the scores are capped and have a bias.  Each keeps its
 // registers and branches out of the others' loop: 1.15 -> 1.01 ms for 65536 tokens
 // of 16 heads without either, 0.51 -> 0.35 ms for 2 x 2048 tokens of 32 heads with a
 // cap (its polynomial in paired operations).
-template <typename T, int DH, bool CAP, bool BIAS>
+template <typename T, int DH, bool CAP, bool BIAS, bool SINGLE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_constant__ Maps maps, int items) {
     using S = TcShape<DH>;
@@ -197,6 +209,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     uint64_t *list_ready = q_free + 1, *list_free = list_ready + 2, *mma_done = list_free + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1), *go_on = abort_flag + 1;
+    float2 *s_join = reinterpret_cast<float2 *>(tmem_slot + 4);       // maximum and sum of the second group's rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.group << p.shift;
@@ -238,7 +251,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     if (warp < kSoftWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ---- softmax: one row per thread ----
-        const int t = warp >> 2;
+        const int t = warp >> 2, thread = SINGLE ? threadIdx.x & (kTileRows - 1) : threadIdx.x;
         const bool docs = p.a.doc_q != nullptr;
         constexpr bool bias = BIAS;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane 32 (warp mod 4), in bits 16-31
@@ -254,13 +267,14 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             const int n_list = ok ? s_n[4 * (it & 1)] : 0;
             const int n = ((n_list << p.shift) + kTileKeys - 1) / kTileKeys;
             const int tiles = tiles_of(unit_of(p, item));
-            if (t < tiles) {
+            const int turns = SINGLE ? (n - t + 1) >> 1 : n;      // tiles of keys of this group
+            if (SINGLE || t < tiles) {
                 int pos, doc, limit, near;
                 const int32_t *doc_k;
                 float slope;
                 {
                     const Unit u = unit_of(p, item);
-                    const Row r0 = row_of(p, u);
+                    const Row r0 = row_of(p, u, thread);
                     pos = r0.pos;
                     doc = docs && r0.valid ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + r0.token] : -1;
                     doc_k = docs ? p.a.doc_k + (size_t)u.b * p.c.nk_tokens : nullptr;
@@ -274,7 +288,8 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     }
                 }
                 float m = -INFINITY, l = 0.f;
-                for (int j = 0; ok && j < n; ++j) {
+                for (int i = 0; ok && i < turns; ++i) {
+                    const int j = SINGLE ? 2 * i + t : i;
                     // what the tile's chunks are to the unit: lane e looks at chunk e; lane i
                     // fetches the documents of keys 4i .. 4i + 3 while S is computed
                     const int per = kTileKeys >> p.shift;
@@ -289,7 +304,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         for (int c = 0; c < 4; ++c)
                             dk[c] = entry >= 0 && at + c < p.c.nk_tokens ? doc_k[at + c] : -1;
                     }
-                    ok = mbar_wait_warp(&s_full[t], (done + j) & 1, abort_flag);
+                    ok = mbar_wait_warp(&s_full[t], (done + i) & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     float s[kTileKeys];
@@ -350,10 +365,10 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     if (__any_sync(kFull, top > m + kSlack)) {
                         const float was = m;
                         m = fmaxf(m, top);
-                        if (j > 0) {
+                        if (i > 0) {
                             const float corr = was == -INFINITY ? 0.f : rr_attn::ex2(was - m);
                             l *= corr;
-                            ok = mbar_wait_warp(&o_done[t], (done + j - 1) & 1, abort_flag);
+                            ok = mbar_wait_warp(&o_done[t], (done + i - 1) & 1, abort_flag);
                             if (!ok) break;
                             tc_fence_after();
                             // 16 columns at a time: the scores hold 128 registers
@@ -396,16 +411,42 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     unpack2(add2(sums[0], sums[1]), sum0, sum1);
                     l += sum0 + sum1;
                 }
-                if (ok && n > 0) {
-                    ok = mbar_wait_warp(&o_done[t], (done + n - 1) & 1, abort_flag);
+                if (ok && turns > 0) {
+                    ok = mbar_wait_warp(&o_done[t], (done + turns - 1) & 1, abort_flag);
                     tc_fence_after();
                 }
-                done += n;
+                done += turns;
+                // the groups' halves of a row: O = O0 2^(m0 - m) + O1 2^(m1 - m), without the
+                // accumulators of a half that saw nothing
+                float from0 = 0.f, from1 = 0.f;
+                bool use0 = false, use1 = false;
+                if constexpr (SINGLE) {
+                    if (t == 1) s_join[thread] = make_float2(m, ok ? l : -1.f);
+                    tc_fence_before();
+                    soft_sync();
+                    tc_fence_after();
+                    if (t == 1) {
+                        soft_sync();         // the first group has read this one's O
+                        tc_fence_after();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&list_free[it & 1]);
+                        continue;
+                    }
+                    const float2 other = s_join[thread];
+                    ok = ok && __all_sync(kFull, other.y != -1.f);
+                    use0 = l != 0.f;
+                    use1 = other.y != 0.f;
+                    const float top = !use1 ? m : !use0 ? other.x : fmaxf(m, other.x);
+                    if (use0) from0 = rr_attn::ex2(m - top);
+                    if (use1) from1 = rr_attn::ex2(other.x - top);
+                    l = (use0 ? l * from0 : 0.f) + (use1 ? other.y * from1 : 0.f);
+                    m = top;
+                }
                 // (worked out again: kept over the loop, it costs registers that the scores need)
                 int again_item = item;
                 asm volatile("" : "+r"(again_item));
                 const Unit u = unit_of(p, again_item);
-                const Row r0 = row_of(p, u);
+                const Row r0 = row_of(p, u, thread);
                 const int row0 = u.tile * kTiles * kTileRows;
                 // A thread writes its row in whole sectors.  A row that saw nothing is zero
                 // whatever its accumulators hold.
@@ -419,6 +460,17 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     if (ok && n > 0) {
                         ld32(o_at + c0, o);
                         wait_ld32(o);
+                        if constexpr (SINGLE) {
+#pragma unroll
+                            for (int c16 = 0; c16 < 32; c16 += 16) {
+                                uint32_t second[16];
+                                if (n > 1) ld16(o_at + 128 + c0 + c16, second);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    o[c16 + c] = (use0 ? o[c16 + c] * from0 : 0.f) +
+                                                 (use1 ? __uint_as_float(second[c]) * from1 : 0.f);
+                            }
+                        }
                     }
                     uint32_t w[16];
 #pragma unroll
@@ -444,6 +496,10 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         !ok ? NAN
                             : l == 0.f ? -INFINITY
                                        : (m - kLift + log2f(l)) * kLn2 - (bias ? p.a.slopes[r0.head] * (float)near : 0.f);
+                if constexpr (SINGLE) {
+                    tc_fence_before();
+                    soft_sync();
+                }
                 // (where the sum is a NaN, a score that the row sees is one, and so is the row)
                 unsigned again = __ballot_sync(kFull, ok && bad && r0.valid && l == l);
                 while (again) {
@@ -519,7 +575,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             constexpr uint32_t kQk = idesc_of<T>(kTileKeys, false), kPv = idesc_of<T>(DH, true);
             const uint32_t base = __shfl_sync(kFull, tmem, 0);
             auto qk = [&](int t, int s) {
-                const uint64_t a = sw128_desc(saddr(q_s) + t * S::kTileBytes), b = sw128_desc(saddr(kv_s) + s * S::kTileBytes);
+                const uint64_t a = sw128_desc(saddr(q_s) + (SINGLE ? 0 : t * S::kTileBytes)), b = sw128_desc(saddr(kv_s) + s * S::kTileBytes);
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk) {
                     const uint64_t off = (uint64_t)((kk >> 2) * (kSubBytes >> 4) + (kk & 3) * 2);
@@ -553,32 +609,63 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 if (!ok) break;
                 ++nq;
                 tc_fence_after();
-                for (int t = 0; t < tiles; ++t) qk(t, g % S::kStages);
-                tc_commit_elect(&empty[g % S::kStages]);
-                if (n == 1) tc_commit_elect(q_free);
-                for (int j = 0; ok && j < n; ++j, g += 2) {
-                    const int gv = g + 1, sv = gv % S::kStages, gk = g + 2, sk = gk % S::kStages;
-                    ok = mbar_wait_warp(&full[sv], (gv / S::kStages) & 1, abort_flag);
-                    if (ok && j + 1 < n) ok = mbar_wait_warp(&full[sk], (gk / S::kStages) & 1, abort_flag);
-                    for (int t = 0; ok && t < tiles; ++t) {
+                if constexpr (SINGLE) {
+                    // S of tile j + 2 after O of tile j, whose P it takes the place of
+                    const int g0 = g;
+                    g += 2 * n;
+                    auto scores = [&](int j) {
+                        const int at = g0 + 2 * j, s = at % S::kStages;
+                        if (j > 0) ok = mbar_wait_warp(&full[s], (at / S::kStages) & 1, abort_flag);
+                        if (!ok) return;
+                        qk(j & 1, s);
+                        tc_commit_elect(&empty[s]);
+                        if (j + 1 == n) tc_commit_elect(q_free);
+                    };
+                    scores(0);
+                    if (n > 1) scores(1);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const int t = j & 1, at = g0 + 2 * j + 1, s = at % S::kStages;
+                        ok = mbar_wait_warp(&full[s], (at / S::kStages) & 1, abort_flag);
                         for (int half = 0; ok && half < 2; ++half) {
-                            ok = mbar_wait_warp(&p_ready[2 * t + half], (done[t] + j) & 1, abort_flag);
+                            ok = mbar_wait_warp(&p_ready[2 * t + half], ((t ? done[1] : done[0]) + (j >> 1)) & 1, abort_flag);
                             if (!ok) break;
                             tc_fence_after();
-                            pv(t, sv, half, j == 0);
+                            pv(t, s, half, j < 2);
                         }
                         if (!ok) break;
-                        if (t == tiles - 1) tc_commit_elect(&empty[sv]);
-                        if (j + 1 < n) {
-                            qk(t, sk);
-                            if (t == tiles - 1) {
-                                tc_commit_elect(&empty[sk]);
-                                if (j + 2 == n) tc_commit_elect(q_free);
+                        tc_commit_elect(&empty[s]);
+                        if (j + 2 < n) scores(j + 2);
+                    }
+                    done[0] += (n + 1) >> 1;
+                    done[1] += n >> 1;
+                } else {
+                    for (int t = 0; t < tiles; ++t) qk(t, g % S::kStages);
+                    tc_commit_elect(&empty[g % S::kStages]);
+                    if (n == 1) tc_commit_elect(q_free);
+                    for (int j = 0; ok && j < n; ++j, g += 2) {
+                        const int gv = g + 1, sv = gv % S::kStages, gk = g + 2, sk = gk % S::kStages;
+                        ok = mbar_wait_warp(&full[sv], (gv / S::kStages) & 1, abort_flag);
+                        if (ok && j + 1 < n) ok = mbar_wait_warp(&full[sk], (gk / S::kStages) & 1, abort_flag);
+                        for (int t = 0; ok && t < tiles; ++t) {
+                            for (int half = 0; ok && half < 2; ++half) {
+                                ok = mbar_wait_warp(&p_ready[2 * t + half], (done[t] + j) & 1, abort_flag);
+                                if (!ok) break;
+                                tc_fence_after();
+                                pv(t, sv, half, j == 0);
+                            }
+                            if (!ok) break;
+                            if (t == tiles - 1) tc_commit_elect(&empty[sv]);
+                            if (j + 1 < n) {
+                                qk(t, sk);
+                                if (t == tiles - 1) {
+                                    tc_commit_elect(&empty[sk]);
+                                    if (j + 2 == n) tc_commit_elect(q_free);
+                                }
                             }
                         }
                     }
+                    for (int t = 0; t < tiles; ++t) done[t] += n;
                 }
-                for (int t = 0; t < tiles; ++t) done[t] += n;
             }
             tc_commit_elect(mma_done);
             const long long t0 = clock64();
@@ -638,7 +725,7 @@ bool tensor_map(const Masked &p, const void *base, int tokens, int heads, const 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int DH, bool CAP, bool BIAS>
+template <typename T, int DH, bool CAP, bool BIAS, bool SINGLE>
 cudaError_t launch_tc_as(const Masked &p, unsigned units, cudaStream_t s) {
     using S = TcShape<DH>;
     static_assert(S::kSmem <= 232448, "shared memory of one CTA");
@@ -648,7 +735,7 @@ cudaError_t launch_tc_as(const Masked &p, unsigned units, cudaStream_t s) {
         !tensor_map(p, p.a.k, c.nk_tokens, c.kv_heads, c.k_stride, c.chunk, &maps.k, &maps.axes[1]) ||
         !tensor_map(p, p.a.v, c.nk_tokens, c.kv_heads, c.v_stride, c.chunk, &maps.v, &maps.axes[2]))
         return cudaErrorNotSupported;
-    auto kern = masked_attention_tc_kernel<T, DH, CAP, BIAS>;
+    auto kern = masked_attention_tc_kernel<T, DH, CAP, BIAS, SINGLE>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = rr_attn::allow_smem(reinterpret_cast<const void *>(kern), S::kSmem, done);
     if (e != cudaSuccess) return e;
@@ -659,17 +746,27 @@ cudaError_t launch_tc_as(const Masked &p, unsigned units, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, int DH, bool CAP, bool BIAS>
+cudaError_t launch_tc_rows(const Masked &p, unsigned units, cudaStream_t s) {
+    return (p.group << p.shift) <= kTileRows ? launch_tc_as<T, DH, CAP, BIAS, true>(p, units, s)
+                                             : launch_tc_as<T, DH, CAP, BIAS, false>(p, units, s);
+}
+
 template <typename T, int DH>
 cudaError_t launch_tc_type(const Masked &p, unsigned units, cudaStream_t s) {
     const bool cap = p.c.soft_cap > 0.f, bias = p.a.slopes != nullptr;
-    if (cap) return bias ? launch_tc_as<T, DH, true, true>(p, units, s) : launch_tc_as<T, DH, true, false>(p, units, s);
-    return bias ? launch_tc_as<T, DH, false, true>(p, units, s) : launch_tc_as<T, DH, false, false>(p, units, s);
+    if (cap) return bias ? launch_tc_rows<T, DH, true, true>(p, units, s) : launch_tc_rows<T, DH, true, false>(p, units, s);
+    return bias ? launch_tc_rows<T, DH, false, true>(p, units, s) : launch_tc_rows<T, DH, false, false>(p, units, s);
 }
 
-// Units that fill a tile of 128 rows: with fewer, the rows that are missing cost as
-// much as those that are there, and mma.sync, at a quarter of the rate, is as fast.
+// A tile of 128 rows costs the same whatever part of it a unit fills, and mma.sync, at
+// a quarter of the rate, pays by the row.  Measured with 8192 tokens, 32 chunks each,
+// here and there: 2048 units of 96 rows 150 and 261 us at dh 64, 189 and 437 at dh
+// 128; of 64 rows 225 and 236 at dh 64 (287 and 266 by chunks of 32), 274 and 398 at
+// dh 128, but with a cap and a bias 559 and 517; of 48 rows 408 and 242, 534 and 486.
 cudaError_t launch_tc(const Masked &p, unsigned units, cudaStream_t s) {
-    if ((p.group << p.shift) < kTileRows || p.c.width < 1) return cudaErrorNotSupported;
+    const int rows = p.group << p.shift;
+    if (rows < 64 || (rows == 64 && (p.c.dh == 64 || p.c.soft_cap > 0.f)) || p.c.width < 1) return cudaErrorNotSupported;
     if (p.c.dtype == RR_BF16)
         return p.c.dh == 64 ? launch_tc_type<__nv_bfloat16, 64>(p, units, s) : launch_tc_type<__nv_bfloat16, 128>(p, units, s);
     return p.c.dh == 64 ? launch_tc_type<__half, 64>(p, units, s) : launch_tc_type<__half, 128>(p, units, s);

@@ -134,6 +134,48 @@ def test_what_masked_rows_hold_is_not_read(rr, dtype, shape):
     assert torch.isfinite(got[0][:, :, :16]).all()
 
 
+# units of one tile of 64 to 128 rows, whose tiles of 128 keys two groups of warps take in turn
+ONE_TILE = [dict(nq=130, chunk=64, width=1), dict(nq=130, chunk=64, width=2), dict(nq=130, chunk=64, width=3),
+            dict(nq=200, chunk=64, width=6, dtype=HF), dict(nq=200, nk=500, chunk=128, dh=128, hq=2, width=4),
+            dict(nq=100, chunk=32, dh=128, hq=6, width=13, dtype=HF), dict(nq=90, chunk=16, hq=14, width=9),
+            dict(nq=190, chunk=64, hq=2, dh=128, width=5), dict(nq=40, nk=700, chunk=16, hq=8, hkv=1, b=1, width=40),
+            dict(nq=1, nk=300, chunk=128, hq=1, hkv=1, width=3)]
+
+
+@pytest.mark.parametrize("kind", ["", "ct", "cs", "cdp", "ctsdp"])
+@pytest.mark.parametrize("shape", range(len(ONE_TILE)))
+def test_units_of_one_tile(rr, shape, kind):
+    s = ONE_TILE[shape]
+    q, k, v, route = make(seed=shape + 50, q_scale=4.0 if "t" in kind else 1.0, **s)
+    kw = masks(kind, q.shape[0], q.shape[1], q.shape[2], k.shape[2])
+    check(rr.masked_attention(q, k, v, route, s["chunk"], return_lse=True, **kw), q, k, v, route, s["chunk"], **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("shape", [dict(chunk=64, nq=190, width=3), dict(chunk=32, hq=8, dh=128, nq=190, width=9),
+                                   dict(chunk=16, hq=12, nq=150, width=30)])
+def test_what_masked_rows_hold_is_not_read_by_units_of_one_tile(rr, dtype, shape):
+    test_what_masked_rows_hold_is_not_read(rr, dtype, shape)
+
+
+def test_halves_of_a_row_that_see_nothing(rr):
+    # of the unit's two tiles of keys the rows of one document see the first alone, of
+    # the other the second, and of a third none; the tiles hold no numbers elsewhere
+    q, k, v, _ = make(b=1, nq=64, nk=256, chunk=64, seed=9)
+    doc_q = (torch.arange(64) % 3)[None].int().to(DEV)
+    doc_k = torch.tensor([0] * 128 + [1] * 128)[None].int().to(DEV)
+    route = torch.arange(4, dtype=torch.int32).expand(1, 2, 1, 4).contiguous().to(DEV)
+    for spoil in (None, 0, 1):
+        if spoil is not None:
+            v[:, :, 128 * spoil + 5] = float("nan")
+            k[:, :, 128 * spoil + 9] = float("inf")
+        got = rr.masked_attention(q, k, v, route, 64, doc_q=doc_q, doc_k=doc_k, return_lse=True)
+        check(got, q, k, v, route, 64, doc_q=doc_q, doc_k=doc_k)
+        assert torch.count_nonzero(got[0][:, :, 2::3]) == 0
+        if spoil == 0:
+            assert torch.isfinite(got[0][:, :, 1::3]).all()
+
+
 def test_rows_that_see_nothing(rr):
     q, k, v, route = make(nq=50, nk=80)
     doc_q = torch.full((2, 50), 3, dtype=torch.int32, device=DEV)
