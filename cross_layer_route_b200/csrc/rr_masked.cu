@@ -1,6 +1,6 @@
 // rr_masked.cu -- masked attention over a route (declared in
 // include/rr_attention.h): the entry point and the kernel on mma.sync, for units
-// of fewer than 128 rows (rr_masked_tc.cu has the others).
+// of up to 64 rows and operands without a tensor map (rr_masked_tc.cu has the others).
 //
 // One CTA = up to 64 rows of a unit (rr_masked.cuh), 16 rows per warp, so the
 // query heads that share a key head read its chunks once.  Keys are visited in

@@ -14,6 +14,7 @@
 //   warp 9          TMA producer: Q, then key chunks gathered by the route into
 //                   tiles of 128 keys, K and V in turn through a ring of stages;
 //   warps 10, 11    the list of key chunks of the next item.
+// (A unit of one row tile has both groups on it, the tiles of keys in turn.)
 // While one tile's softmax runs, the tensor cores work for the other, and the next
 // item's list, queries and first keys arrive while this one ends.  TMEM: two S
 // tiles and two O tiles of 128 columns.  P aliases S: the product that reads it

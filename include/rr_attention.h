@@ -135,8 +135,8 @@ typedef struct {
 
 /* Enqueues the attention.  Scores, softmax and sums are fp32; the weights are
  * rounded to the inputs' type for the product with v, and the result to that
- * type once.  Units of 128 and more rows (q_heads / route_heads * chunk) run on
- * tcgen05, smaller ones on mma.sync; both give the same bits from call to call.
+ * type once.  Units of more than 64 rows (q_heads / route_heads * chunk; at dh 128
+ * without a cap of 64 too) run on tcgen05, smaller ones on mma.sync; both give the same bits from call to call.
  * Rows whose result is not finite take a slow path.  `out` must not
  * overlap the inputs.  Every wait inside the kernels is bounded (about a
  * second); should one run out, the rows not yet written become NaN.  Errors: RR_EINVAL (shape, stride, null or
