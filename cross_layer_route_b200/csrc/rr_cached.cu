@@ -63,7 +63,9 @@ constexpr int ctas_per_sm(int dh, int nt) { return nt * dh <= 128 ? 2 : 1; }
 // kOne: a CTA takes a job.  kCluster: a cluster of CTAs takes a job, kSplits: so do
 // CTAs that leave their parts in the workspace.  kShares: all jobs' steps, laid end
 // to end, are cut into equal shares, one per CTA; a share ends in the middle of a
-// job and may hold several.
+// job and may hold several.  The caller counts the CTAs from the page table's width;
+// sequences that are far shorter can leave fewer steps than CTAs, which then take one
+// each (shares_of), so that no share is empty and a job's shares are neighbours.
 enum { kOne, kCluster, kSplits, kShares };
 constexpr int kMaxShared = 512;  // sequences of a call cut into shares
 
@@ -285,6 +287,9 @@ __device__ __forceinline__ void sum_steps(const Cached &p, int *prefix) {
     __syncthreads();
 }
 
+// The shares that a call of `total` steps is cut into.
+__device__ __forceinline__ int shares_of(const Cached &p, long long total) { return (int)min((long long)p.blocks, total); }
+
 // Two dims of one row's result from its sums: o relative to 2^(n2 - kLift) of the
 // weights', their sum to 2^n1; dim 0's caller writes lse.
 template <int DH>
@@ -331,9 +336,10 @@ cached_attention_kernel(const __grid_constant__ Cached p) {
     if (p.mode == kShares) {
         sum_steps(p, s_prefix);
         const long long total = (long long)s_prefix[p.n.batch] * p.c.heads * p.zs;
-        cur = total * blockIdx.x / p.blocks;
-        stop = total * (blockIdx.x + 1) / p.blocks;
-        if (cur >= stop) return;
+        const int shares = shares_of(p, total);
+        if ((int)blockIdx.x >= shares) return;
+        cur = total * blockIdx.x / shares;
+        stop = total * (blockIdx.x + 1) / shares;
     }
     const int sub_shift = p.shift - 4;                 // steps per chunk
     for (;;) {
@@ -948,8 +954,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const __gr
         const int steps = s_prefix[b + 1] - s_prefix[b];
         const long long total = (long long)s_prefix[p.n.batch] * hz, first = (long long)s_prefix[b] * hz + (long long)in_b * steps;
         // the shares that the job's first and last step are in
-        const int c0 = steps ? (int)(((first + 1) * p.blocks - 1) / total) : 0;
-        parts = steps ? (int)(((first + steps) * p.blocks - 1) / total) - c0 + 1 : 0;
+        const int shares = shares_of(p, total);
+        const int c0 = steps ? (int)(((first + 1) * shares - 1) / total) : 0;
+        parts = steps ? (int)(((first + steps) * shares - 1) / total) - c0 + 1 : 0;
         part = (size_t)c0 + b * hz + in_b;
     }
     const float *at = p.part + (part * kRows + row % kRows) * (DH + kState);

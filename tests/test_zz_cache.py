@@ -302,6 +302,38 @@ def test_ragged_batches(rr, fmt, dh, chunk, heads, group, qt, batch, most):
         check(got, *case, **kw)
 
 
+# tables far wider than the sequences, most of them empty in some: the caller cuts by the
+# table's width, so that there are fewer steps of 16 tokens than blocks (up to 296)
+@pytest.mark.parametrize("fmt,dh,chunk,heads,group,qt,width,lens,routed", [
+    ("e4m3", 128, 64, 8, 4, 1, 2000, [64] * 3, 0), ("e4m3", 128, 64, 8, 4, 1, 64, [500] + [0] * 11, 0),
+    ("e2m1", 64, 32, 1, 4, 1, 64, [20] * 100, 0), ("e4m3", 64, 32, 2, 4, 5, 400, [100, 1, 100, 0, 1, 100, 1, 100], 0),
+    ("e4m3", 128, 16, 4, 8, 4, 400, [20, 0, 0, 1, 100, 100], 0), ("e2m1", 128, 128, 1, 4, 5, 400, [0, 300, 1], 0),
+    ("e2m1", 128, 32, 2, 8, 5, 1000, [1, 1, 0], 0), ("e4m3", 128, 64, 8, 4, 1, 188, [200] + [0] * 62 + [60], 0),
+    ("e4m3", 64, 16, 1, 2, 1, 1000, [128] * 36 + [112], 0), ("e2m1", 64, 16, 1, 2, 1, 1000, [128] * 37, 0),
+    ("e4m3", 64, 16, 1, 2, 1, 1000, [128] * 36 + [129], 0), ("e4m3", 64, 16, 1, 4, 2, 200, [0] * 99 + [700], 150),
+    ("e2m1", 128, 16, 1, 4, 1, 200, [0] * 50 + [700] + [0] * 49, 150), ("e4m3", 64, 32, 2, 4, 5, 60, [0] * 39 + [700], 200),
+    ("e2m1", 128, 16, 2, 8, 4, 900, [0] * 24, 0)])
+def test_few_tokens_under_a_wide_table(rr, fmt, dh, chunk, heads, group, qt, width, lens, routed):
+    batch = len(lens)
+    codes, scales, fmt, q, lens, short = cached_case(lens=lens, fmt=fmt, dh=dh, chunk=chunk, heads=heads, group=group, qt=qt,
+                                                     seed=width)
+    rng = np.random.default_rng(width)
+    table = rng.integers(-1, codes.shape[0], (batch, width)).astype(np.int32)     # pages of others behind a sequence's end
+    for b, n in enumerate(lens):
+        table[b, :-(-n // chunk)] = short[b, :-(-n // chunk)]
+    route = _i32(rng.integers(-1, 800 // chunk, (batch, heads, routed))) if routed else None
+    cfg = rr.rr_cache_config(codes.shape[0], heads, dh, chunk, rr.RR_E4M3 if fmt == "e4m3" else rr.RR_E2M1)
+    attn = rr.rr_cached_attn_config(batch, qt, heads * group, rr.RR_BF16, width, width, routed, max(routed, 1))
+    need = rr.rr_cached_attention_workspace_bytes(cfg, attn, routed > 0)
+    assert need > 0
+    slopes = torch.tensor([2.0 ** -(h + 1) for h in range(heads * group)]).to(DEV)
+    for kw in (dict(), dict(slopes=slopes)):
+        work = torch.full((need,), 255, dtype=torch.uint8, device=DEV)            # NaN wherever nothing is written
+        got = rr.cached_attention(codes, scales, q, _i32(lens), _i32(table), route=route, workspace=work, return_lse=True,
+                                  **kw)
+        check(got, codes, scales, fmt, q, lens, table, route, **kw)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_scales_that_differ_by_many_binades(rr, fmt):
     case = cached_case(lens=[300, 90], fmt=fmt, dh=128, spread=24, q_scale=2.0 ** -24, group=4)
