@@ -591,11 +591,11 @@ def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
     contiguous; seq_lens [batch] int32: cached tokens, the query tokens among
     them; table [batch, width] int32; route: None (every chunk) or contiguous
     int32 [batch, cache heads, stride] of chunk ids, of which the first `width`
-    are read.  Returns (or fills) out like q, contiguous, with return_lse also
-    float32 [batch, q_tokens, q_heads].  `workspace`: uint8 device memory of
-    rr_cached_attention_workspace_bytes, for callers that hold their own; two
-    calls that can run at once need one each.  With a `stream`, the results
-    belong to it."""
+    (default: all) are read; where there are none the result is zero. Returns (or
+    fills) out like q, contiguous, with return_lse also float32 [batch, q_tokens,
+    q_heads]. `workspace`: uint8 device memory of
+    rr_cached_attention_workspace_bytes, for callers that hold their own; two calls
+    that can run at once need one each. With a `stream`, the results belong to it."""
     dtype, shape = q.dtype, q.shape
     if len(shape) != 4 or dtype not in _HALVES:
         raise ValueError(f"q: expected bf16 or f16 [batch, tokens, heads, dh], got {_describe(q)}")
@@ -607,7 +607,8 @@ def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
     stride, d_route = 1, 0
     if route is not None:
         stride = _dim("route", route, 3, 2)
-        d_route = _int32("route", route, (batch, heads, stride), index)
+        # (a route of no entries has no address, which would stand for no route at all; it is not read)
+        d_route = _int32("route", route, (batch, heads, stride), index) or seq_lens.data_ptr()
         width = stride if width is None else int(width)
         if width > stride:
             raise ValueError(f"width {width} is larger than the route's {stride} entries")

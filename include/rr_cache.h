@@ -126,7 +126,7 @@ typedef struct {
     const void *q;              /* [batch, q_tokens, q_heads, dh] by q_stride; 16-byte aligned */
     const int32_t *seq_lens;    /* [batch] */
     const int32_t *page_table;  /* [batch, table_stride] */
-    const int32_t *route;       /* optional [batch, heads, route_stride]; NULL: every chunk */
+    const int32_t *route;       /* optional [batch, heads, route_stride]; NULL: every chunk (width 0: none) */
     const float *slopes;        /* optional [q_heads], in [0, 1e30] */
     void *out;                  /* [batch, q_tokens, q_heads, dh], contiguous; 16-byte aligned */
     float *lse;                 /* optional [batch, q_tokens, q_heads] */

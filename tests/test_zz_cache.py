@@ -420,6 +420,16 @@ def test_sequences_without_tokens_or_pages(rr):
     assert rr.cached_attention(codes, scales, q[:, :0], _i32(lens), _i32(table)).shape == (4, 0, 4, 64)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(width=0)])
+def test_routes_of_no_entries_see_nothing(rr, kw):
+    codes, scales, fmt, q, lens, table = cached_case(lens=[40, 700])
+    for stride in (0,) if not kw else (0, 5):
+        route = torch.zeros(2, 2, stride, dtype=torch.int32, device=DEV)
+        out, lse = rr.cached_attention(codes, scales, q, _i32(lens), _i32(table), route=route, return_lse=True, **kw)
+        assert torch.count_nonzero(out) == 0 and torch.isneginf(lse).all()
+        assert rr.cached_attention(codes, scales, q[:0], _i32([]), _i32(table)[:0], route=route[:0], **kw).shape == (0, 1, 4, 64)
+
+
 def test_bias_of_far_positions_keeps_the_scores(rr):
     # the route names only the far end of a long sequence
     chunk, dh = 128, 64
