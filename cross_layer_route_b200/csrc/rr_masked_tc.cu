@@ -36,7 +36,7 @@
 // (no change), one block per item (1.09 ms), results by TMA (6500 cycles an item, by
 // 32-byte stores 2000).
 //
-// Every wait is bounded; when one runs out the CTA stops, drains its copies,
+// Every wait is bounded (wait_warp); when one runs out the CTA stops, drains its copies,
 // waits for its last MMA, frees TMEM and leaves the rows it has not written NaN.
 #include "rr_masked.cuh"
 #include "rr_tc.cuh"
@@ -179,6 +179,34 @@ __device__ __forceinline__ Row row_of(const Masked &p, const Unit &u, int thread
     return r;
 }
 
+// A bounded wait whose outcome the whole warp shares.  Rows that are computed on their
+// own (row_alone) keep the softmax warps for longer than the bound at the largest
+// widths, while all other roles wait for them: each such row counts itself in `alone`,
+// the second word behind the abort flag, and a wait begins anew where the count has
+// moved.  The longest row, of 131072 keys, takes a twentieth of the bound, and there
+// are only so many rows, so that every wait ends.
+__device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, volatile int *abort_flag) {
+    bool ok = mbar_test(b, parity);
+    if (!ok) {
+        volatile int *alone = abort_flag + 2;
+        long long t0 = clock64();
+        int seen = *alone;
+        while (!(ok = mbar_test_sleep(b, parity))) {
+            if (*abort_flag) break;
+            if (clock64() - t0 > kSpinLimit) {
+                const int now = *alone;
+                if (now == seen) {
+                    *abort_flag = 1;
+                    break;
+                }
+                seen = now;
+                t0 = clock64();
+            }
+        }
+    }
+    return __all_sync(kFull, ok);
+}
+
 // The softmax warps' barrier.
 __device__ __forceinline__ void soft_sync() {
     asm volatile("bar.sync 2, %0;" ::"n"(32 * kSoftWarps) : "memory");
@@ -210,6 +238,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     uint64_t *list_ready = q_free + 1, *list_free = list_ready + 2, *mma_done = list_free + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1), *go_on = abort_flag + 1;
+    int *alone = reinterpret_cast<int *>(tmem_slot + 3);              // rows computed on their own: see wait_warp
     float2 *s_join = reinterpret_cast<float2 *>(tmem_slot + 4);       // maximum and sum of the second group's rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -231,6 +260,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
         mbar_init(q_free, 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
+        *alone = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kSoftWarps) {
@@ -264,7 +294,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
         bool ok = true;
         for (int it = 0, item = blockIdx.x; item < items; ++it, item += gridDim.x) {
             const int32_t *list = s_list + (it & 1) * kMaxWidth;
-            ok = ok && mbar_wait_warp(&list_ready[it & 1], (it >> 1) & 1, abort_flag);
+            ok = ok && wait_warp(&list_ready[it & 1], (it >> 1) & 1, abort_flag);
             const int n_list = ok ? s_n[4 * (it & 1)] : 0;
             const int n = ((n_list << p.shift) + kTileKeys - 1) / kTileKeys;
             const int tiles = tiles_of(unit_of(p, item));
@@ -305,7 +335,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         for (int c = 0; c < 4; ++c)
                             dk[c] = entry >= 0 && at + c < p.c.nk_tokens ? doc_k[at + c] : -1;
                     }
-                    ok = mbar_wait_warp(&s_full[t], (done + i) & 1, abort_flag);
+                    ok = wait_warp(&s_full[t], (done + i) & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     float s[kTileKeys];
@@ -369,7 +399,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         if (i > 0) {
                             const float corr = was == -INFINITY ? 0.f : rr_attn::ex2(was - m);
                             l *= corr;
-                            ok = mbar_wait_warp(&o_done[t], (done + i - 1) & 1, abort_flag);
+                            ok = wait_warp(&o_done[t], (done + i - 1) & 1, abort_flag);
                             if (!ok) break;
                             tc_fence_after();
                             // 16 columns at a time: the scores hold 128 registers
@@ -413,7 +443,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     l += sum0 + sum1;
                 }
                 if (ok && turns > 0) {
-                    ok = mbar_wait_warp(&o_done[t], (done + turns - 1) & 1, abort_flag);
+                    ok = wait_warp(&o_done[t], (done + turns - 1) & 1, abort_flag);
                     tc_fence_after();
                 }
                 done += turns;
@@ -506,6 +536,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 while (again) {
                     const int r = __ffs(again) - 1;
                     again &= again - 1;
+                    if (lane == 0) atomicAdd(alone, 1);
                     row_alone<T, DH>(p, u, list, n_list, row0 + (warp << 5) + r, __shfl_sync(kFull, near, r));
                 }
             }
@@ -522,12 +553,12 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             for (int it = 0, item = blockIdx.x; ok && item < items; ++it, item += gridDim.x) {
                 const Unit u = unit_of(p, item);
                 const int32_t *list = s_list + (it & 1) * kMaxWidth;
-                ok = mbar_wait_warp(&list_ready[it & 1], (it >> 1) & 1, abort_flag);
+                ok = wait_warp(&list_ready[it & 1], (it >> 1) & 1, abort_flag);
                 if (!ok) break;
                 const int n_list = s_n[4 * (it & 1)], n = ((n_list << p.shift) + kTileKeys - 1) / kTileKeys;
                 const int row0 = u.tile * kTiles * kTileRows, tiles = tiles_of(u);
                 if (n > 0) {
-                    ok = mbar_wait_warp(q_free, (nq & 1) ^ 1, abort_flag);
+                    ok = wait_warp(q_free, (nq & 1) ^ 1, abort_flag);
                     if (!ok) break;
                     // the heads of the tiles' rows; rows past the unit as tokens past the last, which read as zeros
                     mbar_expect_tx_elect(q_ready, tiles * S::kTileBytes);
@@ -545,7 +576,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 const int vh = maps.axes[2] & 1 ? u.kv_head : 0, vb = maps.axes[2] & 2 ? u.b : 0;
                 for (int i = 0; i < 2 * n; ++i) {
                     const int s = g % S::kStages;
-                    ok = mbar_wait_warp(&empty[s], ((g / S::kStages) & 1) ^ 1, abort_flag);
+                    ok = wait_warp(&empty[s], ((g / S::kStages) & 1) ^ 1, abort_flag);
                     if (!ok) break;
                     mbar_expect_tx_elect(&full[s], S::kTileBytes);
                     const CUtensorMap *map = i & 1 ? &maps.v : &maps.k;
@@ -599,14 +630,14 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             bool ok = true;
             for (int it = 0, item = blockIdx.x; ok && item < items; ++it, item += gridDim.x) {
                 const Unit u = unit_of(p, item);
-                ok = mbar_wait_warp(&list_ready[it & 1], (it >> 1) & 1, abort_flag);
+                ok = wait_warp(&list_ready[it & 1], (it >> 1) & 1, abort_flag);
                 if (!ok) break;
                 const int n = ((s_n[4 * (it & 1)] << p.shift) + kTileKeys - 1) / kTileKeys, tiles = tiles_of(u);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&list_free[it & 1]);
                 if (n == 0) continue;
-                ok = mbar_wait_warp(q_ready, nq & 1, abort_flag) &&
-                     mbar_wait_warp(&full[g % S::kStages], (g / S::kStages) & 1, abort_flag);
+                ok = wait_warp(q_ready, nq & 1, abort_flag) &&
+                     wait_warp(&full[g % S::kStages], (g / S::kStages) & 1, abort_flag);
                 if (!ok) break;
                 ++nq;
                 tc_fence_after();
@@ -616,7 +647,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     g += 2 * n;
                     auto scores = [&](int j) {
                         const int at = g0 + 2 * j, s = at % S::kStages;
-                        if (j > 0) ok = mbar_wait_warp(&full[s], (at / S::kStages) & 1, abort_flag);
+                        if (j > 0) ok = wait_warp(&full[s], (at / S::kStages) & 1, abort_flag);
                         if (!ok) return;
                         qk(j & 1, s);
                         tc_commit_elect(&empty[s]);
@@ -626,9 +657,9 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     if (n > 1) scores(1);
                     for (int j = 0; ok && j < n; ++j) {
                         const int t = j & 1, at = g0 + 2 * j + 1, s = at % S::kStages;
-                        ok = mbar_wait_warp(&full[s], (at / S::kStages) & 1, abort_flag);
+                        ok = wait_warp(&full[s], (at / S::kStages) & 1, abort_flag);
                         for (int half = 0; ok && half < 2; ++half) {
-                            ok = mbar_wait_warp(&p_ready[2 * t + half], ((t ? done[1] : done[0]) + (j >> 1)) & 1, abort_flag);
+                            ok = wait_warp(&p_ready[2 * t + half], ((t ? done[1] : done[0]) + (j >> 1)) & 1, abort_flag);
                             if (!ok) break;
                             tc_fence_after();
                             pv(t, s, half, j < 2);
@@ -645,11 +676,11 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                     if (n == 1) tc_commit_elect(q_free);
                     for (int j = 0; ok && j < n; ++j, g += 2) {
                         const int gv = g + 1, sv = gv % S::kStages, gk = g + 2, sk = gk % S::kStages;
-                        ok = mbar_wait_warp(&full[sv], (gv / S::kStages) & 1, abort_flag);
-                        if (ok && j + 1 < n) ok = mbar_wait_warp(&full[sk], (gk / S::kStages) & 1, abort_flag);
+                        ok = wait_warp(&full[sv], (gv / S::kStages) & 1, abort_flag);
+                        if (ok && j + 1 < n) ok = wait_warp(&full[sk], (gk / S::kStages) & 1, abort_flag);
                         for (int t = 0; ok && t < tiles; ++t) {
                             for (int half = 0; ok && half < 2; ++half) {
-                                ok = mbar_wait_warp(&p_ready[2 * t + half], (done[t] + j) & 1, abort_flag);
+                                ok = wait_warp(&p_ready[2 * t + half], (done[t] + j) & 1, abort_flag);
                                 if (!ok) break;
                                 tc_fence_after();
                                 pv(t, sv, half, j == 0);
@@ -678,7 +709,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
             const PartTeam<32 * (kSoftWarps + 2), 64, 1> team;
             for (int it = 0, item = blockIdx.x; item < items; ++it, item += gridDim.x) {
                 if (warp == kSoftWarps + 2) {
-                    const bool ok = mbar_wait_warp(&list_free[it & 1], ((it >> 1) & 1) ^ 1, abort_flag);
+                    const bool ok = wait_warp(&list_free[it & 1], ((it >> 1) & 1) ^ 1, abort_flag);
                     if (lane == 0) *go_on = ok;
                 }
                 team.sync();

@@ -137,9 +137,11 @@ typedef struct {
  * rounded to the inputs' type for the product with v, and the result to that
  * type once.  Units of more than 64 rows (q_heads / route_heads * chunk; at dh 128
  * without a cap of 64 too) run on tcgen05, smaller ones on mma.sync; both give the same bits from call to call.
- * Rows whose result is not finite take a slow path.  `out` must not
+ * Rows whose result is not finite, and rows whose route's chunks hold an infinity or
+ * a NaN in a value row that they do not see, take a slow path: 610 cycles a key and
+ * row at dh 128, hundreds of times the usual.  `out` must not
  * overlap the inputs.  Every wait inside the kernels is bounded (about a
- * second); should one run out, the rows not yet written become NaN.  Errors: RR_EINVAL (shape, stride, null or
+ * second without progress); should one run out, the rows not yet written become NaN.  Errors: RR_EINVAL (shape, stride, null or
  * misaligned pointer), RR_ECUDA (launch). */
 rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const rr_masked_attn_args *args,
                               void *stream);

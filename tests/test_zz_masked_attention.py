@@ -176,6 +176,24 @@ def test_halves_of_a_row_that_see_nothing(rr):
             assert torch.isfinite(got[0][:, :, 1::3]).all()
 
 
+@pytest.mark.parametrize("hq", [1, 2])
+def test_blocks_outlast_rows_computed_on_their_own(rr, hq):
+    # the first unit's rows, at the widest route, meet a NaN in a value row that nobody sees
+    # and take 1.3 s; the rest of their block's units, the last one among them, come after
+    chunk, nqc, width, dh = 128, 149, 1024, 128
+    q, k, v, _ = make(b=1, hq=hq, hkv=1, nq=nqc * chunk, nk=4 * chunk, dh=dh, chunk=chunk, seed=11)
+    route = torch.full((1, 1, nqc, width), -1, dtype=torch.int32)
+    route[:, :, 0] = torch.arange(width) % 4
+    route[:, :, 1:, 0] = torch.arange(1, nqc) % 3 + 1
+    doc = torch.zeros(1, 4 * chunk, dtype=torch.int32)
+    doc[:, 5] = -1
+    v[:, :, 5] = float("nan")
+    kw = dict(doc_q=torch.zeros(1, nqc * chunk, dtype=torch.int32, device=DEV), doc_k=doc.to(DEV))
+    got = rr.masked_attention(q, k, v, route.to(DEV), chunk, return_lse=True, **kw)
+    assert torch.isfinite(got[0]).all()
+    check(got, q, k, v, route, chunk, **kw)
+
+
 def test_rows_that_see_nothing(rr):
     q, k, v, route = make(nq=50, nk=80)
     doc_q = torch.full((2, 50), 3, dtype=torch.int32, device=DEV)
