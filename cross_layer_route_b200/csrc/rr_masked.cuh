@@ -197,8 +197,7 @@ __device__ __forceinline__ int nearest(const Masked &p, const Unit &u, const int
 // own result is not finite; both end here with the right values.  32 keys at a time:
 // a lane scores one, then the warp adds their values, a lane DH / 32 dims.  Measured:
 // 610 cycles a key at dh 128 and 380 at dh 64, in all 0.2 s for a warp's 32 rows of
-// 16384 keys and 1.3 s for 131072, the most that a route holds, which is more than the
-// other roles' waits last by themselves (wait_warp in rr_masked_tc.cu).
+// 16384 keys and 1.3 s for 131072, the most that a route holds.
 // `row` numbers the unit's rows.
 template <typename T, int DH>
 __device__ __forceinline__ void row_alone(const Masked &p, const Unit &u, const int32_t *list, int n, int row, int near) {

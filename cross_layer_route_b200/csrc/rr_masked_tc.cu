@@ -36,7 +36,7 @@
 // (no change), one block per item (1.09 ms), results by TMA (6500 cycles an item, by
 // 32-byte stores 2000).
 //
-// Every wait is bounded (wait_warp); when one runs out the CTA stops, drains its copies,
+// Every wait is bounded (kWaitLimit); when one runs out the CTA stops, drains its copies,
 // waits for its last MMA, frees TMEM and leaves the rows it has not written NaN.
 #include "rr_masked.cuh"
 #include "rr_tc.cuh"
@@ -61,6 +61,11 @@ constexpr int kSoftRegs = 224, kOtherRegs = 56;
 constexpr float kSlack = 8.f;     // growth of the maximum that is let pass
 constexpr float kLift = 7.f;      // weights are 2^7 at the maximum
 constexpr int kSubBytes = kTileRows * 128;    // 128 rows of 64 elements
+// Cycles that a wait lasts at most, 8.7 s.  While a softmax warp computes rows on their
+// own (row_alone), all other roles wait for it: 32 rows of the widest route's 131072 keys
+// at the 610 cycles a key that they take out of L2 are 1.3 s, at 4096 a key the limit.
+// (Waits of a second that such rows prolong made capped scores 2 to 5 % slower.)
+constexpr long long kWaitLimit = 1ll << 34;
 
 
 template <int DH>
@@ -179,32 +184,9 @@ __device__ __forceinline__ Row row_of(const Masked &p, const Unit &u, int thread
     return r;
 }
 
-// A bounded wait whose outcome the whole warp shares.  Rows that are computed on their
-// own (row_alone) keep the softmax warps for longer than the bound at the largest
-// widths, while all other roles wait for them: each such row counts itself in `alone`,
-// the second word behind the abort flag, and a wait begins anew where the count has
-// moved.  The longest row, of 131072 keys, takes a twentieth of the bound, and there
-// are only so many rows, so that every wait ends.
+// A bounded wait whose outcome the whole warp shares.
 __device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, volatile int *abort_flag) {
-    bool ok = mbar_test(b, parity);
-    if (!ok) {
-        volatile int *alone = abort_flag + 2;
-        long long t0 = clock64();
-        int seen = *alone;
-        while (!(ok = mbar_test_sleep(b, parity))) {
-            if (*abort_flag) break;
-            if (clock64() - t0 > kSpinLimit) {
-                const int now = *alone;
-                if (now == seen) {
-                    *abort_flag = 1;
-                    break;
-                }
-                seen = now;
-                t0 = clock64();
-            }
-        }
-    }
-    return __all_sync(kFull, ok);
+    return __all_sync(kFull, mbar_wait(b, parity, abort_flag, kWaitLimit));
 }
 
 // The softmax warps' barrier.
@@ -238,7 +220,6 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
     uint64_t *list_ready = q_free + 1, *list_free = list_ready + 2, *mma_done = list_free + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1), *go_on = abort_flag + 1;
-    int *alone = reinterpret_cast<int *>(tmem_slot + 3);              // rows computed on their own: see wait_warp
     float2 *s_join = reinterpret_cast<float2 *>(tmem_slot + 4);       // maximum and sum of the second group's rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -260,7 +241,6 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
         mbar_init(q_free, 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
-        *alone = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kSoftWarps) {
@@ -536,7 +516,6 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                 while (again) {
                     const int r = __ffs(again) - 1;
                     again &= again - 1;
-                    if (lane == 0) atomicAdd(alone, 1);
                     row_alone<T, DH>(p, u, list, n_list, row0 + (warp << 5) + r, __shfl_sync(kFull, near, r));
                 }
             }

@@ -133,16 +133,17 @@ typedef struct {
     float *lse;              /* optional [batch, q_heads, nq_tokens] */
 } rr_masked_attn_args;
 
-/* Enqueues the attention.  Scores, softmax and sums are fp32; the weights are
+/* Enqueues the attention. Scores, softmax and sums are fp32; the weights are
  * rounded to the inputs' type for the product with v, and the result to that
- * type once.  Units of more than 64 rows (q_heads / route_heads * chunk; at dh 128
- * without a cap of 64 too) run on tcgen05, smaller ones on mma.sync; both give the same bits from call to call.
- * Rows whose result is not finite, and rows whose route's chunks hold an infinity or
- * a NaN in a value row that they do not see, take a slow path: 610 cycles a key and
- * row at dh 128, hundreds of times the usual.  `out` must not
- * overlap the inputs.  Every wait inside the kernels is bounded (about a
- * second without progress); should one run out, the rows not yet written become NaN.  Errors: RR_EINVAL (shape, stride, null or
- * misaligned pointer), RR_ECUDA (launch). */
+ * type once. Units of more than 64 rows (q_heads / route_heads * chunk; at dh
+ * 128 without a cap of 64 too) run on tcgen05, smaller ones on mma.sync; both
+ * give the same bits from call to call. Rows whose result is not finite, and
+ * rows whose route's chunks hold an infinity or a NaN in a value row that they
+ * do not see, take a slow path: 610 cycles a key and row at dh 128, hundreds of
+ * times the usual. `out` must not overlap the inputs. Every wait inside the
+ * kernels is bounded (by one second to nine); should one run out, the rows not
+ * yet written become NaN. Errors: RR_EINVAL (shape, stride, null or misaligned
+ * pointer), RR_ECUDA (launch). */
 rr_status rr_masked_attention(const rr_masked_attn_config *cfg, const rr_masked_attn_args *args,
                               void *stream);
 
