@@ -296,9 +296,11 @@ template <int DH>
 __device__ __forceinline__ void write_out(const Cached &p, int b, int head, int row, int dim, float x, float y, float n1,
                                           float sum, float n2, float near) {
     const bool none = sum == 0.f;
-    const float f = none ? 0.f : ex2(n2 - kLift) / sum;
-    x = none ? 0.f : x * f;
-    y = none ? 0.f : y * f;
+    // (the power in two factors: values' scales reach down to 2^-127, in 4 bits another
+    // kGroupLift below, and ex2 has no results below 2^-126)
+    const float half = ex2(0.5f * (n2 - kLift)), f = half / sum;
+    x = none ? 0.f : x * f * half;
+    y = none ? 0.f : y * f * half;
     const size_t orow = ((size_t)b * p.n.q_tokens + row / p.group) * p.n.q_heads + head * p.group + row % p.group;
     static_cast<uint32_t *>(p.a.out)[(orow * DH + dim) / 2] = p.n.dtype == RR_BF16 ? pack_bf16(x, y) : pack_f16(x, y);
     if (p.a.lse && dim == 0)

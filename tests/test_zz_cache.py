@@ -387,6 +387,23 @@ def test_queries_and_keys_at_the_ends_of_their_range(rr, fmt, power):
     check(got, codes, scales, fmt, q, lens, table)
 
 
+@pytest.mark.parametrize("lens", [[48, 96], [9000, 4000]])      # whole jobs, and joined parts
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_values_at_the_small_end_of_their_range(rr, fmt, lens):
+    # values' scales down to 2^-126: their results are numbers of bf16 (and what cache_read returns)
+    codes, scales, fmt, q, lens, table = cached_case(lens=lens, fmt=fmt, dh=64, group=4, heads=1)
+    ref, ref_lse, mean = M.cached_attention(codes.cpu().numpy(), scales.cpu().numpy(), fmt, _np(q), np.array(lens), table)
+    values = scales[:, :, 1]
+    down = int(values[values != 255].min()) - 1
+    assert 100 < down < 126
+    scales[:, :, 1] = torch.where(values == 255, values, values - down)
+    out = _np(rr.cached_attention(codes, scales, q, _i32(lens), _i32(table))) * 2.0 ** down
+    # as in check(), delta below 2^-24 (64 + 8) 8 max |q| max |k|; and half a step of bf16's smallest numbers, 2^-134
+    delta = 2.0 ** -24 * 72 * 8 * float(q.abs().max()) * 64
+    bound = (2 * delta + 2.0 ** -11 + 2.0 ** -12) * mean + 2.0 ** -8 * np.abs(ref) + max(lens) * 2.0 ** -32 * 64 + 2.0 ** (down - 134)
+    assert (np.abs(out - ref) <= bound).all(), np.abs(out - ref).max()
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_groups_that_hold_no_number(rr, fmt):
     # a NaN scale reaches the rows that see it, of its own dims for the values, and no others
