@@ -164,6 +164,7 @@ struct Half<__nv_bfloat16> {
         mma_bf16(d, a, b0, b1);
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16(lo, hi); }
+    static __device__ __forceinline__ uint32_t pack_mean(float lo, float hi) { return pack_bf16(lo, hi); }
     static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
 };
@@ -174,6 +175,14 @@ struct Half<__half> {
         mma_f16(d, a, b0, b1);
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_f16(lo, hi); }
+    // Means of finite values, which are at most 65504.  Weights rounded up by 2^-11 at most
+    // can carry them past 65520, from where on f16 has infinities.  A NaN stays one.  (In
+    // bf16 the sums of such values are infinite before.)
+    static __device__ __forceinline__ uint32_t pack_mean(float lo, float hi) {
+        const __half2 top = __float2half2_rn(65504.f);
+        const __half2 x = __hmax2_nan(__hmin2_nan(__floats2half2_rn(lo, hi), top), __hneg2(top));
+        return *reinterpret_cast<const uint32_t *>(&x);
+    }
     static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
     static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
 };

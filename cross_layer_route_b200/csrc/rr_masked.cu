@@ -392,8 +392,8 @@ masked_attention_kernel(const __grid_constant__ Masked p, const __grid_constant_
     uint32_t *o1 = reinterpret_cast<uint32_t *>(out + (token + 8) * p.c.out_stride[2]);
 #pragma unroll
     for (int nd = 0; nd < DH / 8; ++nd) {
-        if (ok0) o0[nd * 4 + t] = l0 == 0.f ? 0u : Half<T>::pack(o[nd][0] * inv0, o[nd][1] * inv0);
-        if (ok1) o1[nd * 4 + t] = l1 == 0.f ? 0u : Half<T>::pack(o[nd][2] * inv1, o[nd][3] * inv1);
+        if (ok0) o0[nd * 4 + t] = l0 == 0.f ? 0u : Half<T>::pack_mean(o[nd][0] * inv0, o[nd][1] * inv0);
+        if (ok1) o1[nd * 4 + t] = l1 == 0.f ? 0u : Half<T>::pack_mean(o[nd][2] * inv1, o[nd][3] * inv1);
     }
     if (p.a.lse && t == 0) {
         float *lse = p.a.lse + ((size_t)u.b * p.c.q_heads + head) * p.c.nq_tokens + token;

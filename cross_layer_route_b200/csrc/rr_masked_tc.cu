@@ -489,7 +489,7 @@ masked_attention_tc_kernel(const __grid_constant__ Masked p, const __grid_consta
                         if (!ok) o[2 * c] = o[2 * c + 1] = NAN;
                         else if (l == 0.f) o[2 * c] = o[2 * c + 1] = 0.f;
                         bad = bad || !isfinite(o[2 * c]) || !isfinite(o[2 * c + 1]);
-                        w[c] = Half<T>::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
+                        w[c] = Half<T>::pack_mean(o[2 * c] * inv, o[2 * c + 1] * inv);
                     }
                     if (r0.valid) {
                         if (out32) {

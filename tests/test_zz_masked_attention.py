@@ -13,6 +13,8 @@ rounded once to the inputs' type (half a step: eps / 2 of it; f16 weights below
 with 2^-12 of slack on the first factor for the fp32 sums of weights.
 The log of the sum: delta + 2^-21 (1 + |lse|).
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -132,6 +134,29 @@ def test_what_masked_rows_hold_is_not_read(rr, dtype, shape):
     got = rr.masked_attention(q, k, v, route, chunk, return_lse=True, **kw)
     check(got, q, k, v, route, chunk, **kw)
     assert torch.isfinite(got[0][:, :, :16]).all()
+
+
+@pytest.mark.parametrize("chunk,hq,dh", [(16, 2, 64), (64, 4, 64), (64, 8, 128)])
+def test_means_at_the_top_of_f16(rr, chunk, hq, dh):
+    # weights of 2^6 (1 + 1.2 2^-11), which f16 rounds up to 2^6 (1 + 2^-10), and one of 2^7:
+    # their product with values of 65504 over their sum is 65529, past the last number of f16
+    q, k, v, _ = make(b=1, hq=hq, hkv=2, nq=64, nk=256, dh=dh, chunk=chunk, dtype=HF)
+    route = torch.arange(256 // chunk, dtype=torch.int32).expand(1, 2, 64 // chunk, -1).contiguous().to(DEV)
+    q.zero_()
+    k.zero_()
+    q[..., 0], k[:, :, 1:, 0] = 1.0, -1.0
+    v.fill_(65504.0)
+    v[..., 1::2] = -65504.0
+    scale = math.log(2.0 / (1.0 + 1.2 * 2.0 ** -11))
+    kw = dict(scale=scale)
+    got = rr.masked_attention(q, k, v, route, chunk, return_lse=True, **kw)
+    assert torch.isfinite(got[0]).all()
+    check(got, q, k, v, route, chunk, **kw)
+    k[0, 0, 3, 0] = float("nan")      # a NaN is not a large number
+    v[0, 1, 3, 1] = float("inf")
+    got = rr.masked_attention(q, k, v, route, chunk, return_lse=True, **kw)
+    assert torch.isnan(got[0][:, :hq // 2]).all() and (got[0][:, hq // 2:, :, 1] == float("inf")).all()
+    assert torch.isfinite(got[0][:, hq // 2:, :, 2:]).all()
 
 
 # units of one tile of 64 to 128 rows, whose tiles of 128 keys two groups of warps take in turn
