@@ -159,6 +159,21 @@ def test_means_at_the_top_of_f16(rr, chunk, hq, dh):
     assert torch.isfinite(got[0][:, hq // 2:, :, 2:]).all()
 
 
+@pytest.mark.parametrize("chunk,hq,dh", [(16, 2, 64), (64, 4, 64), (64, 8, 128)])
+def test_means_at_the_top_of_bf16(rr, chunk, hq, dh):
+    # sums of such values pass the last number of fp32, their means do not
+    q, k, v, route = make(b=1, hq=hq, hkv=2, nq=130, dh=dh, chunk=chunk, seed=7)
+    top = float(torch.finfo(BF).max)
+    v.copy_(v.clamp(-3, 3) * 2.0 ** 126)
+    v[:, :, 20:90] = top
+    v[:, :, 20:90, 1::2] = -top
+    v[:, :, :, 2] = 2.0 ** -100
+    for kw in (dict(), dict(causal=True)):
+        got = rr.masked_attention(q, k, v, route, chunk, return_lse=True, **kw)
+        assert torch.isfinite(got[0]).all() and (got[0][..., 2] <= 2.0 ** -100).all()
+        check(got, q, k, v, route, chunk, **kw)
+
+
 # units of one tile of 64 to 128 rows, whose tiles of 128 keys two groups of warps take in turn
 ONE_TILE = [dict(nq=130, chunk=64, width=1), dict(nq=130, chunk=64, width=2), dict(nq=130, chunk=64, width=3),
             dict(nq=200, chunk=64, width=6, dtype=HF), dict(nq=200, nk=500, chunk=128, dh=128, hq=2, width=4),
