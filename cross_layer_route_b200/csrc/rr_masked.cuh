@@ -203,6 +203,7 @@ template <typename T, int DH>
 __device__ __forceinline__ void row_alone(const Masked &p, const Unit &u, const int32_t *list, int n, int row, int near) {
     constexpr int E = DH / 32;
     const int lane = threadIdx.x & 31;
+    __syncwarp();     // other lanes have stored the row that is stored anew below
     const int head = u.route_head * p.group + (row >> p.shift), token = (u.i << p.shift) + (row & (p.c.chunk - 1));
     const int pos = p.c.q_offset + token;
     const T *q = static_cast<const T *>(p.a.q) + u.b * p.c.q_stride[0] + head * p.c.q_stride[1] + token * p.c.q_stride[2];
