@@ -14,6 +14,9 @@ with 2^-12 of slack on the first factor for the fp32 sums of weights.
 The log of the sum: delta + 2^-21 (1 + |lse|).
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -329,6 +332,39 @@ def test_streams_and_graphs(rr, shape):
     graph.replay()
     torch.cuda.synchronize()
     check((out, lse), q, k, v, route, chunk, causal=True)
+
+
+FIRST_CALLS = """
+import threading
+import torch
+import cross_layer_route_b200 as rr
+torch.cuda.set_device(0)
+g = torch.Generator().manual_seed(1)
+q, k, v = (torch.randn(1, 2, 256, 64, generator=g).to(torch.bfloat16).cuda() for _ in range(3))
+route = torch.arange(2, dtype=torch.int32).expand(1, 2, 2, 2).contiguous().cuda()
+torch.cuda.synchronize()
+start, got = threading.Barrier(16), [None] * 16
+def call(i):
+    stream = torch.cuda.Stream()
+    start.wait()
+    got[i] = rr.masked_attention(q, k, v, route, 128, causal=True, return_lse=True, stream=stream)
+threads = [threading.Thread(target=call, args=(i,)) for i in range(16)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+want = rr.masked_attention(q, k, v, route, 128, causal=True, return_lse=True)
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for r in got for x, y in zip(r, want))
+print("same bits")
+"""
+
+
+def test_first_calls_of_many_threads_give_the_same_bits():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=120)
+        assert run.returncode == 0 and "same bits" in run.stdout, run.stderr[-2000:]
 
 
 def test_two_calls_give_the_same_bits(rr):
