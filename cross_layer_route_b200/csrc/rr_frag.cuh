@@ -27,6 +27,24 @@ inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
     return e;
 }
 
+// Whether the rows (of `row` elements) of an output lie apart: by dimensions (at most
+// 3, strides >= 0) from the smallest stride up, each steps over all that the ones
+// before it span.  A size of one counts nothing.
+inline bool rows_apart(const int32_t *size, const int64_t *stride, int dims, int64_t row) {
+    bool used[3] = {};
+    __int128 span = row;
+    for (int n = 0; n < dims; ++n) {
+        int least = -1;
+        for (int i = 0; i < dims; ++i)
+            if (!used[i] && size[i] > 1 && (least < 0 || stride[i] < stride[least])) least = i;
+        if (least < 0) break;
+        if (stride[least] < span) return false;
+        used[least] = true;
+        span += (__int128)(size[least] - 1) * stride[least];
+    }
+    return true;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -471,9 +471,8 @@ bool config_ok(const rr_masked_attn_config *c) {
         !strides_ok(c->v_stride, c->batch, c->kv_heads, c->nk_tokens) ||
         !strides_ok(c->out_stride, c->batch, c->q_heads, c->nq_tokens))
         return false;
-    const int out_sizes[3] = {c->batch, c->q_heads, c->nq_tokens};
-    for (int i = 0; i < 3; ++i)
-        if (out_sizes[i] > 1 && c->out_stride[i] == 0) return false;
+    const int32_t out_sizes[3] = {c->batch, c->q_heads, c->nq_tokens};
+    if (!rr_attn::rows_apart(out_sizes, c->out_stride, 3, c->dh)) return false;
     const long long group = c->q_heads / c->route_heads, chunks = (c->nq_tokens + c->chunk - 1) / c->chunk;
     const long long heads = (long long)c->batch * c->route_heads, rows16 = group * c->chunk / 16;
     if (group * c->chunk > 1 << 24) return false;

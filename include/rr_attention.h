@@ -96,7 +96,9 @@ rr_status rr_sparse_attention(const rr_attn_config *cfg, const void *d_q, const 
  * and q_offset + nq_tokens, nk_tokens <= 2^24 (positions are exact in fp32);
  * scale >= 0 and at most 1e30; soft_cap 0 or in [1e-3, 1e30]; rows of a unit,
  * q_heads / route_heads * chunk, <= 2^24, and 16ths of them times batch * route_heads *
- * query chunks <= 2^31 - 1; strides in elements, >= 0 and multiples of 8 (of `out` > 0); those of a size of one count nothing. */
+ * query chunks <= 2^31 - 1; strides in elements, >= 0 and multiples of 8; those of a size of one count nothing.  The
+ * rows of `out` lie apart: by dimensions from the smallest stride up, each stride
+ * is at least what the ones before it span. */
 typedef struct {
     int32_t batch;
     int32_t q_heads;      /* query (and output) heads */

@@ -76,6 +76,29 @@ def test_strides_of_a_size_of_one_count_nothing():
             attn_args(), 0, 0, 0)
 
 
+@pytest.mark.parametrize("out", [(51200, 6400, 8), (51200, 64, 64), (6400, 6400, 64), (51200, 6392, 64), (51192, 6400, 64),
+                                 (1 << 40, 1 << 40, 64)])
+def test_masked_attention_refuses_results_on_top_of_one_another(out):
+    refused(rr.rr_masked_attention, masked_cfg(out_stride=out), masked_args(), 0)
+
+
+@pytest.mark.parametrize("none", ["batch", "nq_tokens"])
+def test_masked_attention_takes_results_in_any_order(none):
+    # two dimensions at a time: calls of nothing return after the check of the others' strides
+    n0, n1, d0, d1 = (2, 8, 0, 1) if none == "nq_tokens" else (8, 100, 1, 2)
+    for s0, s1 in ((64 * n1, 64), (64, 64 * n0), (64 * n1 + 8, 64), (72, 72 * n0), (1 << 40, 64), (64 * n1 - 8, 64), (64, 64),
+                   (64, 64 * n0 - 8), (56, 1 << 20), (1 << 20, 8), (128, 192)):
+        out = [8] * 3
+        out[d0], out[d1] = s0, s1
+        places = sorted(i * s0 + j * s1 for i in range(n0) for j in range(n1))
+        apart = min(y - x for x, y in zip(places, places[1:])) >= 64
+        cfg = masked_cfg(out_stride=tuple(out), **{none: 0})
+        if apart:
+            rr.rr_masked_attention(cfg, masked_args(), 0)
+        else:
+            refused(rr.rr_masked_attention, cfg, masked_args(), 0)
+
+
 def test_masked_attention_with_nothing_to_do():
     rr.rr_masked_attention(masked_cfg(batch=0), masked_args(), 0)
     rr.rr_masked_attention(masked_cfg(nq_tokens=0), masked_args(q=0, out=0), 0)
