@@ -343,8 +343,9 @@ rr_status run(const rr_cache_config *cfg, const rr_cache_pool *pool, const rr_ca
             const int64_t x = stride[i][j];
             if ((j == 0 ? rows->rows : cfg->heads) <= 1) continue;
             if (x < 0 || x > (1ll << 40) || x * size % 16 != 0) return RR_EINVAL;
-            if (!write && x < cfg->dh) return RR_EINVAL;
         }
+        const int32_t sizes[2] = {rows->rows, cfg->heads};
+        if (!write && !rr_attn::rows_apart(sizes, stride[i], 2, cfg->dh)) return RR_EINVAL;
     }
     if (rows->rows == 0 || rows->batch == 0 || (!k && !v)) return RR_OK;
     if (cfg->pages > 0 && (!pool->codes || !pool->scales || !aligned(pool->codes, 16) || !aligned(pool->scales, 16)))

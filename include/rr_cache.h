@@ -85,7 +85,9 @@ rr_status rr_cache_write(const rr_cache_config *cfg, const rr_cache_pool *pool, 
 
 /* Reads the rows back as `dtype` (rounded to nearest where its range or
  * precision is short of the stored value).  Either output may be NULL.  Rows
- * that belong to no sequence are left as they were.  Errors as above. */
+ * that belong to no sequence are left as they were.  The rows of an output lie
+ * apart: the smaller stride is at least dh, the other at least what the smaller
+ * one's dimension spans.  Errors as above. */
 rr_status rr_cache_read(const rr_cache_config *cfg, const rr_cache_pool *pool, const rr_cache_rows *rows,
                         void *d_k, const int64_t k_stride[2], void *d_v, const int64_t v_stride[2],
                         int32_t dtype, void *stream);

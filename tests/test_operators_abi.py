@@ -155,6 +155,19 @@ def test_cache_rows_refusals():
     rr.rr_cache_read(cache(), pool, rows(), None, s, None, s, rr.RR_BF16, 0)
 
 
+def test_cache_read_refuses_results_on_top_of_one_another():
+    # rows [30, 4] of 64; a call of no sequences returns after the check of the strides
+    pool, s = rr.rr_cache_pool(P, P), (256, 64)
+    for bad in ((248, 64), (64, 64), (192, 64), (64, 64 * 29), (256, 56), (56, 1 << 20), (128, 192)):
+        for k, v in ((bad, s), (s, bad)):
+            refused(rr.rr_cache_read, cache(), pool, rows(batch=0), P, k, P, v, rr.RR_BF16, 0)
+        rr.rr_cache_write(cache(), pool, rows(batch=0), P, bad, P, bad, rr.RR_BF16, 0)      # read only: any
+    for good in ((256, 64), (512, 64), (320, 72), (64, 64 * 30), (72, 72 * 30), (1 << 40, 64), (128, 128 * 29 + 64)):
+        rr.rr_cache_read(cache(), pool, rows(batch=0), P, good, P, good, rr.RR_BF16, 0)
+    rr.rr_cache_read(cache(heads=1), pool, rows(batch=0), P, (64, 0), P, (64, 8), rr.RR_BF16, 0)
+    rr.rr_cache_read(cache(), pool, rows(rows=1, batch=0), P, (0, 64), P, (8, 64), rr.RR_BF16, 0)
+
+
 def attn(**kw):
     base = dict(batch=2, q_tokens=1, q_heads=8, dtype=rr.RR_BF16, table_width=64, table_stride=64, width=0,
                 route_stride=1, scale=0.0, soft_cap=0.0, q_stride=(512, 512, 64))
