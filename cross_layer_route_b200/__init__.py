@@ -387,6 +387,14 @@ for _fmt, _structure in ((_MASKED_CFG, rr_masked_attn_config), (_MASKED_ARGS, rr
     assert _fmt.size == ctypes.sizeof(_structure), _structure
 
 
+def _pack(fmt, *values):
+    """A structure's bytes; ValueError where a value is no number of its field's type."""
+    try:
+        return fmt.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is out of range: {e}") from None
+
+
 def _on_stream(index: int, stream, call, *args):
     """call(stream handle, *args) with CUDA device `index` current and, where the
     caller names a stream, that stream too, so that what the call allocates
@@ -485,7 +493,7 @@ def _masked_attention(handle, q, out, return_lse, ints, ptrs):
     if out is None:
         out = torch.empty_like(q)
     lse = q.new_empty(tuple(shape[:3]), dtype=torch.float32) if return_lse else None
-    status = _lib.rr_masked_attention(_MASKED_CFG.pack(*ints, *out.stride()[:-1]),
+    status = _lib.rr_masked_attention(_pack(_MASKED_CFG, *ints, *out.stride()[:-1]),
                                       _MASKED_ARGS.pack(*ptrs, out.data_ptr(), lse.data_ptr() if return_lse else 0),
                                       handle)
     if status:
@@ -529,8 +537,8 @@ def cache_empty(pages: int, heads: int, chunk: int, dh: int, fmt: str = "e4m3", 
 def _ragged(rows, cu, start, table, index):
     batch, width = _dim("table", table, 2, 0), table.shape[1]
     d_table = _int32("table", table, (batch, width), index)
-    return _CACHE_ROWS.pack(batch, rows, _int32("cu", cu, (batch + 1,), index),
-                            _int32("start", start, (batch,), index), d_table, width, max(width, 1))
+    return _pack(_CACHE_ROWS, batch, rows, _int32("cu", cu, (batch + 1,), index),
+                 _int32("start", start, (batch,), index), d_table, width, max(width, 1))
 
 
 def cache_write(codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
@@ -619,7 +627,7 @@ def cached_attention(codes: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
     if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.get_device() != index
                                   or not workspace.is_contiguous()):
         raise ValueError(f"workspace: expected contiguous uint8 on cuda:{index}, got {_describe(workspace)}")
-    attn = _CACHED_CFG.pack(batch, q_tokens, q_heads, _DTYPES[dtype], table_width, max(table_width, 1), width or 0,
+    attn = _pack(_CACHED_CFG, batch, q_tokens, q_heads, _DTYPES[dtype], table_width, max(table_width, 1), width or 0,
                             max(stride, 1), 0.0 if scale is None else scale, soft_cap, *q_strides)
     ptrs = (q.data_ptr(), _int32("seq_lens", seq_lens, (batch,), index), d_table, d_route,
             _slopes(slopes, q_heads, index))

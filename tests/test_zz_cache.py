@@ -588,3 +588,13 @@ def test_binding_refuses_wrong_tensors(rr):
         rr.cache_read(codes, scales, cu, start, tb, 10, 96)
     with pytest.raises(ValueError):
         rr.cache_read(codes, scales, cu, start, tb, 10, 64, BF, out=(k, k[:9]))
+
+
+def test_numbers_that_fit_no_field_are_refused(rr):
+    codes, scales, fmt, q, lens, table = cached_case()
+    for kw, error in ((dict(scale="1"), ValueError), (dict(soft_cap=10 ** 400), ValueError), (dict(soft_cap=1e39), rr.RRError),
+                      (dict(scale=-1e300), rr.RRError)):
+        with pytest.raises(error):
+            rr.cached_attention(codes, scales, q, _i32(lens), _i32(table), **kw)
+    with pytest.raises(ValueError):
+        rr.cache_read(codes, scales, _i32([0, 1]), _i32([0]), _i32([[0]]), 1 << 31, 64)

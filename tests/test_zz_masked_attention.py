@@ -463,3 +463,13 @@ def test_binding_refuses_wrong_tensors(rr):
         rr.masked_attention(odd, k, v, route, 16)
     with pytest.raises((rr.RRError, ValueError)):
         rr.masked_attention(q, k, v, route, 24)
+
+
+def test_numbers_that_fit_no_field_are_refused(rr):
+    q, k, v, route = make()
+    for kw in (dict(q_offset=1 << 31), dict(q_offset=-(1 << 40)), dict(q_offset=2.5), dict(scale="1"), dict(soft_cap=10 ** 400)):
+        with pytest.raises(ValueError):
+            rr.masked_attention(q, k, v, route, 16, **kw)
+    for kw in (dict(soft_cap=1e39), dict(scale=-1e300)):      # infinities in fp32
+        with pytest.raises(rr.RRError):
+            rr.masked_attention(q, k, v, route, 16, **kw)
