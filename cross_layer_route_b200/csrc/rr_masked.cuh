@@ -212,7 +212,8 @@ __device__ __forceinline__ void row_alone(const Masked &p, const Unit &u, const 
     const int doc = p.a.doc_q ? p.a.doc_q[(size_t)u.b * p.c.nq_tokens + token] : 0;
     const float slope = p.a.slopes ? p.a.slopes[head] * kLog2e : 0.f;
     // weights of at most 2^-18, of at most 2^17 keys: their sums with finite values are finite
-    constexpr float kSmall = 18.f;
+    // (the least, 2^-126 before, does not become zero: it may be an infinity's)
+    constexpr float kSmall = 1.f / (1 << 18);
     static_assert(kMaxWidth * 128 <= 1 << 17, "keys of a route");
     float o[E], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -243,7 +244,7 @@ __device__ __forceinline__ void row_alone(const Masked &p, const Unit &u, const 
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
         const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
-        const float corr = rr_attn::ex2(m - base), w = rr_attn::ex2(x - base - kSmall);
+        const float corr = rr_attn::ex2(m - base), w = rr_attn::ex2(x - base) * kSmall;
         m = mn;
         float sum = w;
 #pragma unroll

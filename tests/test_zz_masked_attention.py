@@ -177,6 +177,21 @@ def test_means_at_the_top_of_bf16(rr, chunk, hq, dh):
         check(got, q, k, v, route, chunk, **kw)
 
 
+@pytest.mark.parametrize("chunk,hq,dh", [(16, 2, 64), (64, 4, 64), (64, 8, 128)])
+def test_infinities_of_small_weights(rr, chunk, hq, dh):
+    # a weight of 2^-120 times an infinity is one
+    q, k, v, _ = make(b=1, hq=hq, hkv=2, nq=64, dh=dh, chunk=chunk)
+    route = torch.arange(64 // chunk, dtype=torch.int32).expand(1, 2, 64 // chunk, -1).contiguous().to(DEV)
+    q.zero_()
+    k.zero_()
+    q[..., 0], k[:, :, 9, 0] = 1.0, -120.0
+    v[:, :, 9, 5], v[:, :, 9, 6] = float("inf"), float("-inf")
+    kw = dict(scale=math.log(2.0))
+    got = rr.masked_attention(q, k, v, route, chunk, return_lse=True, **kw)
+    check(got, q, k, v, route, chunk, **kw)
+    assert (got[0][..., 5] == float("inf")).all() and (got[0][..., 6] == float("-inf")).all()
+
+
 # units of one tile of 64 to 128 rows, whose tiles of 128 keys two groups of warps take in turn
 ONE_TILE = [dict(nq=130, chunk=64, width=1), dict(nq=130, chunk=64, width=2), dict(nq=130, chunk=64, width=3),
             dict(nq=200, chunk=64, width=6, dtype=HF), dict(nq=200, nk=500, chunk=128, dh=128, hq=2, width=4),
